@@ -18,6 +18,8 @@ __all__ = [
     "GdrError", "lib", "status_string", "prepare_chunks", "causal_conv", "chunk_prefill",
     "chunk_prefill_noalloc", "chunk_prefill_slots", "prefill_schedule", "prefill_workspace", "linear", "prefill_fused_workspace", "prefill_window",
     "decode_step", "decode_step_slots", "gated_rmsnorm", "get_device_error", "debug_wait_timeout",
+    "decay_attn_prefill", "decay_attn_prefill_slots", "decay_attn_workspace", "decay_attn_decode",
+    "decay_attn_decode_slots", "block_norm",
     "HEAD_DIM", "CHUNK",
 ]
 
@@ -41,6 +43,16 @@ class FuseArgs(ctypes.Structure):
     """Mirror of ``gdr_prefill_fuse_t``."""
     _fields_ = [("x", _vp), ("conv_w", _vp), ("conv_state_in", _vp), ("conv_state_out", _vp),
                 ("z", _vp), ("norm_w", _vp), ("eps", ctypes.c_float), ("y", _vp)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    """Mirror of ``gdr_block_norm_t``."""
+    _fields_ = [("x", _vp), ("x_stride", ctypes.c_int64), ("post_norm", ctypes.c_int), ("w_post", _vp),
+                ("eps_post", ctypes.c_float), ("gate", _vp), ("gate_stride", ctypes.c_int64),
+                ("gate_shared", ctypes.c_int), ("alpha", ctypes.c_float), ("residual", _vp),
+                ("residual_stride", ctypes.c_int64), ("residual_fp32", ctypes.c_int), ("residual_out", _vp),
+                ("residual_out_stride", ctypes.c_int64), ("w_pre", _vp), ("eps_pre", ctypes.c_float), ("y", _vp),
+                ("y_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -92,6 +104,23 @@ def lib(path: Optional[str] = None):
     L.gdr_linear.argtypes = [_vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp]
     L.gdr_chunk_prefill_schedule.argtypes = [_ip, ctypes.c_int, ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
                                              ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
+    i64 = ctypes.c_int64
+    L.gdr_decay_attn_prefill.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
+                                         ctypes.c_int, _vp, _ip, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                         _vp]
+    L.gdr_decay_attn_prefill_slots.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
+                                               ctypes.c_int, _vp, _ip, ctypes.c_int, _vp, ctypes.c_int, _vp,
+                                               ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
+    L.gdr_decay_attn_decode.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
+                                        ctypes.c_int, _vp, _vp, ctypes.c_int, _vp]
+    L.gdr_decay_attn_decode_slots.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
+                                              ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp]
+    L.gdr_decay_attn_prefill_workspace_size.restype = ctypes.c_size_t
+    L.gdr_decay_attn_prefill_workspace_size.argtypes = [_ip, ctypes.c_int, ctypes.c_int]
+    L.gdr_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), i64, i64, _vp]
+    for fn in ("gdr_decay_attn_prefill", "gdr_decay_attn_prefill_slots", "gdr_decay_attn_decode",
+               "gdr_decay_attn_decode_slots", "gdr_block_norm"):
+        getattr(L, fn).restype = ctypes.c_int
     for fn in ("gdr_prepare_chunks", "gdr_causal_conv", "gdr_chunk_prefill", "gdr_decode_step",
                "gdr_decode_step_slots", "gdr_gated_rmsnorm", "gdr_get_device_error",
                "gdr_debug_wait_timeout", "gdr_chunk_prefill_slots", "gdr_chunk_prefill_schedule", "gdr_linear"):
@@ -424,6 +453,202 @@ def linear(x, w, y=None, stream=None):
         _check("gdr_linear", lib().gdr_linear(_ptr(x, bf, "x"), _ptr(w, bf, "w"), _ptr(y, bf, "y"), int(M), int(N),
                                               int(K), _stream(stream, dev)))
     return y
+
+
+def _heads(t, name, rows, heads=None):
+    """(pointer, token stride) of a bf16 [rows, heads, 128] CUDA tensor whose last two dims are dense."""
+    torch = _torch()
+    ptr = _ptr(t, torch.bfloat16, name, rows=True)
+    if t.shape[2] != HEAD_DIM or t.shape[0] < rows or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {HEAD_DIM}], got {tuple(t.shape)}")
+    # the stride of a dimension of one row means nothing: take it as dense
+    return ptr, (int(t.stride(0)) if t.shape[0] > 1 else 0)
+
+
+def _decay_inputs(q, k, v, log_decay, rows):
+    """Checked arguments shared by the decayed linear attention calls, in the ABI's order."""
+    torch = _torch()
+    (qp, qs), (vp, vs) = _heads(q, "q", rows), _heads(v, "v", rows)
+    hk, hv = int(q.shape[1]), int(v.shape[1])
+    kp, ks = _heads(k, "k", rows, hk)
+    if tuple(log_decay.shape) != (hv,):
+        raise ValueError(f"log_decay must have shape ({hv},), got {tuple(log_decay.shape)}")
+    return (qp, kp, vp, qs, ks, vs, _ptr(log_decay, torch.float32, "log_decay")), hk, hv
+
+
+def _states(t, name, entries, hv):
+    """Pointer of an fp32 [entries, hv, 128, 128] CUDA tensor (None passes)."""
+    if t is not None and tuple(t.shape) != (entries, hv, HEAD_DIM, HEAD_DIM):
+        raise ValueError(f"{name} must be [{entries}, {hv}, {HEAD_DIM}, {HEAD_DIM}], got {tuple(t.shape)}")
+    return _ptr(t, _torch().float32, name)
+
+
+def _decay_o(o, v, hv, rows):
+    torch = _torch()
+    if o is None:
+        o = torch.empty((v.shape[0], hv, HEAD_DIM), dtype=torch.bfloat16, device=v.device)
+    elif o.dim() != 3 or o.shape[0] < rows or tuple(o.shape[1:]) != (hv, HEAD_DIM):
+        raise ValueError(f"o must be [{rows}, {hv}, {HEAD_DIM}], got {tuple(o.shape)}")
+    return o
+
+
+def _slot_ptr(slot, rows):
+    if tuple(slot.shape) != (rows,):
+        raise ValueError(f"slot must have shape ({rows},), got {tuple(slot.shape)}")
+    return _ptr(slot, _torch().int32, "slot")
+
+
+def decay_attn_workspace(cu_seqlens_host, hv: int, device):
+    """A torch uint8 device buffer sized for gdr_decay_attn_prefill, or None when it needs none."""
+    torch = _torch()
+    cu, cup = _host_cu(cu_seqlens_host)
+    nbytes = int(lib().gdr_decay_attn_prefill_workspace_size(cup, cu.shape[0] - 1, int(hv)))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, o, workspace):
+    torch = _torch()
+    cu, cup = _host_cu(cu_seqlens_host)
+    if cu.ndim != 1 or cu.shape[0] < 1:
+        raise ValueError("cu_seqlens_host must hold n_seqs + 1 offsets")
+    if tuple(cu_seqlens.shape) != cu.shape:
+        raise ValueError(f"cu_seqlens must have shape {cu.shape}, got {tuple(cu_seqlens.shape)}")
+    ins, hk, hv = _decay_inputs(q, k, v, log_decay, int(cu[-1]))
+    o = _decay_o(o, v, hv, int(cu[-1]))
+    if workspace is None:
+        workspace = decay_attn_workspace(cu, hv, v.device)
+    ws = (_ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else int(workspace.numel()))
+    return ins, hk, hv, cu, cup, o, workspace, ws
+
+
+def decay_attn_prefill(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, h0=None, hT=None, o=None,
+                       scale: float = 1.0, workspace=None, stream=None):
+    """Decayed linear attention over packed sequences: H_t = exp(log_decay) H_{t-1} + k_t v_t^T,
+    o_t = scale H_t^T q_t.  q, k [T, hk, 128], v [T, hv, 128] bf16 (token-strided views allowed),
+    log_decay [hv] fp32.  Returns o [T, hv, 128] bf16 (and writes hT [N, hv, 128, 128] fp32 when
+    given); rows of o behind the last sequence are left as they were."""
+    torch = _torch()
+    ins, hk, hv, cu, cup, o, workspace, ws = _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host,
+                                                                  o, workspace)
+    n = cu.shape[0] - 1
+    dev = _device_of(q, k, v, log_decay, cu_seqlens, h0, hT, o, workspace)
+    with torch.cuda.device(dev):
+        _check("gdr_decay_attn_prefill", lib().gdr_decay_attn_prefill(
+            *ins, float(scale), hk, hv, _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cup, n,
+            _states(h0, "h0", n, hv), _states(hT, "hT", n, hv), _ptr(o, torch.bfloat16, "o"), *ws,
+            _stream(stream, dev)))
+    return o
+
+
+def decay_attn_prefill_slots(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, state_pool, slot,
+                             init_from_pool: bool = False, o=None, scale: float = 1.0, workspace=None,
+                             stream=None):
+    """decay_attn_prefill on a pool of cached states: sequence n starts from entry slot[n] of
+    state_pool (or from zero, init_from_pool=False) and leaves its final state there.  A slot
+    outside the pool is a sequence that starts from zero and keeps no state."""
+    torch = _torch()
+    ins, hk, hv, cu, cup, o, workspace, ws = _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host,
+                                                                  o, workspace)
+    n, n_slots = cu.shape[0] - 1, int(state_pool.shape[0])
+    dev = _device_of(q, k, v, log_decay, cu_seqlens, state_pool, slot, o, workspace)
+    with torch.cuda.device(dev):
+        _check("gdr_decay_attn_prefill_slots", lib().gdr_decay_attn_prefill_slots(
+            *ins, float(scale), hk, hv, _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cup, n,
+            _states(state_pool, "state_pool", n_slots, hv), n_slots, _slot_ptr(slot, n),
+            int(bool(init_from_pool)), _ptr(o, torch.bfloat16, "o"), *ws, _stream(stream, dev)))
+    return o
+
+
+def decay_attn_decode(q, k, v, log_decay, state, o=None, scale: float = 1.0, stream=None):
+    """One token of decayed linear attention for each of B sequences; q, k [B, hk, 128],
+    v [B, hv, 128] bf16, state [B, hv, 128, 128] fp32 updated in place -> o [B, hv, 128] bf16."""
+    torch = _torch()
+    B = int(v.shape[0])
+    ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
+    o = _decay_o(o, v, hv, B)
+    dev = _device_of(q, k, v, log_decay, state, o)
+    with torch.cuda.device(dev):
+        _check("gdr_decay_attn_decode", lib().gdr_decay_attn_decode(
+            *ins, float(scale), hk, hv, _states(state, "state", B, hv), _ptr(o, torch.bfloat16, "o"), B,
+            _stream(stream, dev)))
+    return o
+
+
+def decay_attn_decode_slots(q, k, v, log_decay, state_pool, slot, o=None, scale: float = 1.0, stream=None):
+    """decay_attn_decode on a pool of cached states: row i updates entry slot[i] in place; a slot
+    outside the pool is a padding row (zero o)."""
+    torch = _torch()
+    B, n_slots = int(v.shape[0]), int(state_pool.shape[0])
+    ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
+    o = _decay_o(o, v, hv, B)
+    dev = _device_of(q, k, v, log_decay, state_pool, slot, o)
+    with torch.cuda.device(dev):
+        _check("gdr_decay_attn_decode_slots", lib().gdr_decay_attn_decode_slots(
+            *ins, float(scale), hk, hv, _states(state_pool, "state_pool", n_slots, hv), n_slots,
+            _slot_ptr(slot, B), _ptr(o, torch.bfloat16, "o"), B, _stream(stream, dev)))
+    return o
+
+
+def _row_view(t, name, dtype, rows, d):
+    """(pointer, row stride) of a CUDA tensor of `rows` rows of d values: contiguous, or [rows, d]
+    with dense rows.  (None, 0) for None."""
+    if t is None:
+        return None, 0
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.numel() != rows * d or t.shape[-1] != d:
+        raise ValueError(f"{name} must hold {rows} rows of {d} values, got {tuple(t.shape)}")
+    if t.dim() == 2 and t.stride(1) == 1 and rows > 1 and not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.stride(0) < d:
+            raise ValueError(f"{name} must have rows that do not overlap")
+        return t.data_ptr(), int(t.stride(0))
+    return _ptr(t, dtype, name), 0
+
+
+def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None, w_pre=None, alpha: float = 1.0,
+               eps: float = 1e-6, eps_post: Optional[float] = None, residual_out=None, y=None,
+               want_residual: bool = True, want_y: bool = True, stream=None):
+    """The norms after and before a block with its gate and residual, row by row:
+    u = x / rms(x) * w_post (post_norm) or x, r = residual + alpha * gate * u,
+    y = r / rms(r) * w_pre.  x, y bf16 [..., d]; gate bf16 [d] or like x; residual and
+    residual_out bf16 or fp32 (like each other).  Returns (residual_out, y); residual_out may be
+    residual and y may be x (in place).  want_residual / want_y = False leaves that output out
+    (None) when no tensor is given for it."""
+    torch = _torch()
+    bf, f32 = torch.bfloat16, torch.float32
+    d = int(x.shape[-1])
+    rows = x.numel() // d if d else 0
+    rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else bf
+    if rdt not in (bf, f32):
+        raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {rdt}")
+    if residual_out is None and want_residual:
+        residual_out = torch.empty(x.shape, dtype=rdt, device=x.device)
+    if y is None and want_y:
+        y = torch.empty(x.shape, dtype=bf, device=x.device)
+    a = BlockNormArgs()
+    a.x, a.x_stride = _row_view(x, "x", bf, rows, d)
+    a.post_norm, a.eps_post = int(bool(post_norm)), float(eps if eps_post is None else eps_post)
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None and tuple(w.shape) != (d,):
+            raise ValueError(f"{name} must have shape ({d},), got {tuple(w.shape)}")
+        setattr(a, name, _ptr(w, f32, name))
+    if gate is not None and gate.dim() == 1:
+        a.gate, _ = _row_view(gate, "gate", bf, 1, d)
+        a.gate_shared = 1
+    else:
+        a.gate, a.gate_stride = _row_view(gate, "gate", bf, rows, d)
+    a.alpha, a.eps_pre = float(alpha), float(eps)
+    a.residual, a.residual_stride = _row_view(residual, "residual", rdt, rows, d)
+    a.residual_out, a.residual_out_stride = _row_view(residual_out, "residual_out", rdt, rows, d)
+    a.residual_fp32 = int(rdt == f32)
+    a.y, a.y_stride = _row_view(y, "y", bf, rows, d)
+    dev = _device_of(x, residual, gate, w_post, w_pre, residual_out, y)
+    with torch.cuda.device(dev):
+        _check("gdr_block_norm", lib().gdr_block_norm(ctypes.byref(a), rows, d, _stream(stream, dev)))
+    return residual_out, y
 
 
 def gated_rmsnorm(o, z, w=None, eps: float = 1e-6, y=None, stream=None):

@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["gdr_host.cu", "conv.cu", "rmsnorm.cu", "decode.cu", "prefill.cu", "prefill_noalloc.cu", "diag.cu",
-           "linear.cu"]
+           "linear.cu", "decay_attn.cu", "decay_decode.cu", "block_norm.cu"]
 LIB = os.path.join(HERE, "libgdr.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

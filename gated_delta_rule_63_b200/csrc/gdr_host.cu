@@ -367,4 +367,215 @@ int gdr_chunk_prefill_slots(const void *q, const void *k, const void *v, int64_t
                               workspace, workspace_bytes, static_cast<cudaStream_t>(stream), &pool);
 }
 
+// ---------------------------------------------------------------------------
+// decayed linear attention
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kStateElems = static_cast<int64_t>(kHeadDim) * kHeadDim;
+
+// Bytes from the first value to behind the last of `rows` rows of `width` values of `size`
+// bytes, `stride` values apart; 0 for no row.
+size_t span_bytes(int64_t rows, int64_t stride, int64_t width, size_t size) {
+  return rows <= 0 ? 0 : (static_cast<size_t>(rows - 1) * stride + width) * size;
+}
+
+// Token strides of q, k, v: 0 is dense; otherwise at least a row and a multiple of 8.
+int decay_strides(int hk, int hv, int64_t *qs, int64_t *ks, int64_t *vs) {
+  const int64_t qk = static_cast<int64_t>(hk) * kHeadDim, vv = static_cast<int64_t>(hv) * kHeadDim;
+  if (*qs == 0) *qs = qk;
+  if (*ks == 0) *ks = qk;
+  if (*vs == 0) *vs = vv;
+  if (*qs < qk || *ks < qk || *vs < vv) return GDR_ERR_SHAPE;
+  if (*qs % 8 != 0 || *ks % 8 != 0 || *vs % 8 != 0) return GDR_ERR_ALIGN;
+  return GDR_OK;
+}
+
+// `out` (bytes long) overlaps q, k or v of `rows` tokens
+bool meets_inputs(const void *out, size_t bytes, const void *q, const void *k, const void *v, int64_t rows,
+                  int64_t qs, int64_t ks, int64_t vs, int hk, int hv) {
+  return overlaps(out, bytes, q, span_bytes(rows, qs, static_cast<int64_t>(hk) * kHeadDim, 2)) ||
+         overlaps(out, bytes, k, span_bytes(rows, ks, static_cast<int64_t>(hk) * kHeadDim, 2)) ||
+         overlaps(out, bytes, v, span_bytes(rows, vs, static_cast<int64_t>(hv) * kHeadDim, 2));
+}
+
+int decay_prefill(const void *q, const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
+                  const float *log_decay, float scale, int hk, int hv, const int32_t *cu_dev,
+                  const int32_t *cu_host, int n_seqs, const DecayStates &st, void *o, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+  int rc = decay_strides(hk, hv, &qs, &ks, &vs);
+  if (rc) return rc;
+  const int total = cu_host[n_seqs];
+  if (!cu_dev || !log_decay) return GDR_ERR_NULL;
+  if (total > 0 && (!q || !k || !v || !o)) return GDR_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(st.h0) ||
+      !aligned16(st.hT) || !aligned16(st.pool) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(st.slot) & 3u) != 0)
+    return GDR_ERR_ALIGN;
+  const size_t o_bytes = static_cast<size_t>(total) * hv * kHeadDim * 2;
+  const size_t need = decay_prefill_workspace_bytes(cu_host, n_seqs, hv);
+  if (need != 0 && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+  const size_t st_bytes = static_cast<size_t>(st.slot ? st.n_slots : n_seqs) * hv * kStateElems * 4;
+  float *st_out = st.slot ? st.pool : st.hT;
+  if (meets_inputs(o, o_bytes, q, k, v, total, qs, ks, vs, hk, hv) ||
+      meets_inputs(st_out, st_bytes, q, k, v, total, qs, ks, vs, hk, hv) ||
+      meets_inputs(workspace, need, q, k, v, total, qs, ks, vs, hk, hv) ||
+      overlaps(o, o_bytes, st_out, st_bytes) || overlaps(o, o_bytes, st.h0, st_bytes) ||
+      overlaps(workspace, need, o, o_bytes) || overlaps(workspace, need, st_out, st_bytes) ||
+      overlaps(workspace, need, st.h0, st_bytes) || (st.h0 != st.hT && overlaps(st.h0, st_bytes, st.hT, st_bytes)))
+    return GDR_ERR_ALIAS;
+  return launch_decay_prefill(q, k, v, qs, ks, vs, log_decay, scale, hk, hv, cu_dev, cu_host, n_seqs, st, o,
+                              workspace, static_cast<cudaStream_t>(stream));
+}
+
+int decay_decode(const void *q, const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
+                 const float *log_decay, float scale, int hk, int hv, float *state, const int32_t *slot, int entries,
+                 void *o, int batch, void *stream) {
+  int rc = decay_strides(hk, hv, &qs, &ks, &vs);
+  if (rc) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(o) ||
+      (reinterpret_cast<uintptr_t>(slot) & 3u) != 0)
+    return GDR_ERR_ALIGN;
+  if (batch > 65535) return GDR_ERR_SHAPE;
+  const size_t o_bytes = static_cast<size_t>(batch) * hv * kHeadDim * 2;
+  const size_t st_bytes = static_cast<size_t>(entries) * hv * kStateElems * 4;
+  if (meets_inputs(o, o_bytes, q, k, v, batch, qs, ks, vs, hk, hv) ||
+      meets_inputs(state, st_bytes, q, k, v, batch, qs, ks, vs, hk, hv) || overlaps(o, o_bytes, state, st_bytes))
+    return GDR_ERR_ALIAS;
+  return launch_decay_decode(q, k, v, qs, ks, vs, log_decay, scale, hk, hv, state, slot, entries, o, batch,
+                             static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+size_t gdr_decay_attn_prefill_workspace_size(const int32_t *cu_host, int n_seqs, int hv) {
+  if (!cu_host || n_seqs <= 0 || hv <= 0 || check_cu_seqlens(cu_host, n_seqs)) return 0;
+  return decay_prefill_workspace_bytes(cu_host, n_seqs, hv);
+}
+
+int gdr_decay_attn_prefill(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float *log_decay, float scale, int hk, int hv,
+                           const int32_t *cu_dev, const int32_t *cu_host, int n_seqs, const float *h0, float *hT,
+                           void *o, void *workspace, size_t workspace_bytes, void *stream) {
+  clear_last_error();
+  int st = check_heads(hk, hv);
+  if (st) return st;
+  if (!cu_host) return GDR_ERR_NULL;
+  st = check_cu_seqlens(cu_host, n_seqs);
+  if (st) return st;
+  if (n_seqs == 0 || (cu_host[n_seqs] == 0 && !hT)) return GDR_OK;   // nothing to compute, nothing to write
+  const DecayStates states{h0, hT, nullptr, nullptr, 0, 0};
+  return decay_prefill(q, k, v, q_stride, k_stride, v_stride, log_decay, scale, hk, hv, cu_dev, cu_host, n_seqs,
+                       states, o, workspace, workspace_bytes, stream);
+}
+
+int gdr_decay_attn_prefill_slots(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float *log_decay, float scale, int hk, int hv,
+                                 const int32_t *cu_dev, const int32_t *cu_host, int n_seqs, float *state_pool,
+                                 int n_slots, const int32_t *slot, int init_from_pool, void *o, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  clear_last_error();
+  int st = check_heads(hk, hv);
+  if (st) return st;
+  if (n_slots < 0 || (init_from_pool != 0 && init_from_pool != 1)) return GDR_ERR_SHAPE;
+  if (!cu_host) return GDR_ERR_NULL;
+  st = check_cu_seqlens(cu_host, n_seqs);
+  if (st) return st;
+  if (n_seqs == 0) return GDR_OK;
+  if (!slot || (n_slots > 0 && !state_pool)) return GDR_ERR_NULL;
+  if (n_slots == 0 && cu_host[n_seqs] == 0) return GDR_OK;
+  const DecayStates states{nullptr, nullptr, slot, state_pool, n_slots, init_from_pool};
+  return decay_prefill(q, k, v, q_stride, k_stride, v_stride, log_decay, scale, hk, hv, cu_dev, cu_host, n_seqs,
+                       states, o, workspace, workspace_bytes, stream);
+}
+
+int gdr_decay_attn_decode(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, const float *log_decay, float scale, int hk, int hv, float *state,
+                          void *o, int batch, void *stream) {
+  clear_last_error();
+  int st = check_heads(hk, hv);
+  if (st) return st;
+  if (batch < 0) return GDR_ERR_SHAPE;
+  if (batch == 0) return GDR_OK;
+  if (!q || !k || !v || !log_decay || !state || !o) return GDR_ERR_NULL;
+  return decay_decode(q, k, v, q_stride, k_stride, v_stride, log_decay, scale, hk, hv, state, nullptr, batch, o,
+                      batch, stream);
+}
+
+int gdr_decay_attn_decode_slots(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, const float *log_decay, float scale, int hk, int hv,
+                                float *state_pool, int n_slots, const int32_t *slot, void *o, int batch,
+                                void *stream) {
+  clear_last_error();
+  int st = check_heads(hk, hv);
+  if (st) return st;
+  if (batch < 0 || n_slots < 0) return GDR_ERR_SHAPE;
+  if (batch == 0) return GDR_OK;
+  if (!q || !k || !v || !log_decay || !slot || !o) return GDR_ERR_NULL;
+  if (n_slots > 0 && !state_pool) return GDR_ERR_NULL;
+  return decay_decode(q, k, v, q_stride, k_stride, v_stride, log_decay, scale, hk, hv, state_pool, slot, n_slots, o,
+                      batch, stream);
+}
+
+// ---------------------------------------------------------------------------
+// norms around a block
+// ---------------------------------------------------------------------------
+int gdr_block_norm(const gdr_block_norm_t *a, int64_t rows, int64_t d, void *stream) {
+  clear_last_error();
+  if (!a) return GDR_ERR_NULL;
+  if (rows < 0 || d <= 0 || d % 8 != 0) return GDR_ERR_SHAPE;
+  if (d > 32768) return GDR_ERR_UNSUPPORTED;
+  if ((a->post_norm != 0 && a->post_norm != 1) || (a->residual_fp32 != 0 && a->residual_fp32 != 1) ||
+      (a->gate_shared != 0 && a->gate_shared != 1))
+    return GDR_ERR_SHAPE;
+  if (!(a->eps_post >= 0.0f) || !(a->eps_pre >= 0.0f)) return GDR_ERR_SHAPE;
+  if (a->w_post && !a->post_norm) return GDR_ERR_SHAPE;   // a weight for a norm that is not asked for
+  if (a->w_pre && !a->y) return GDR_ERR_SHAPE;
+  if (rows == 0) return GDR_OK;
+  if (!a->x || (!a->residual_out && !a->y)) return GDR_ERR_NULL;
+  BlockNormParams p;
+  p.d = static_cast<int>(d);
+  p.x_stride = a->x_stride ? a->x_stride : d;
+  p.gate_stride = a->gate_shared ? 0 : (a->gate_stride ? a->gate_stride : d);
+  p.res_stride = a->residual_stride ? a->residual_stride : d;
+  p.out_stride = a->residual_out_stride ? a->residual_out_stride : d;
+  p.y_stride = a->y_stride ? a->y_stride : d;
+  const int64_t strides[5] = {p.x_stride, p.gate_stride, p.res_stride, p.out_stride, p.y_stride};
+  for (int i = 0; i < 5; ++i) {
+    if (strides[i] < d && !(i == 1 && a->gate_shared)) return GDR_ERR_SHAPE;
+    if (strides[i] % 8 != 0) return GDR_ERR_ALIGN;
+  }
+  if (!aligned16(a->x) || !aligned16(a->w_post) || !aligned16(a->gate) || !aligned16(a->residual) ||
+      !aligned16(a->residual_out) || !aligned16(a->w_pre) || !aligned16(a->y))
+    return GDR_ERR_ALIGN;
+  const size_t rs = a->residual_fp32 ? 4 : 2;
+  const size_t xb = span_bytes(rows, p.x_stride, d, 2), yb = span_bytes(rows, p.y_stride, d, 2);
+  const size_t gb = a->gate_shared ? static_cast<size_t>(d) * 2 : span_bytes(rows, p.gate_stride, d, 2);
+  const size_t ib = span_bytes(rows, p.res_stride, d, rs), ob = span_bytes(rows, p.out_stride, d, rs);
+  const size_t wb = static_cast<size_t>(d) * 4;
+  // in place where every value is read by the thread that writes it: residual_out on residual, y on x
+  const bool res_in_place = a->residual == a->residual_out && p.res_stride == p.out_stride;
+  const bool y_in_place = static_cast<const void *>(a->y) == a->x && p.y_stride == p.x_stride;
+  if (overlaps(a->y, yb, a->residual_out, ob) || overlaps(a->y, yb, a->residual, ib) ||
+      overlaps(a->y, yb, a->gate, gb) || overlaps(a->y, yb, a->w_post, wb) || overlaps(a->y, yb, a->w_pre, wb) ||
+      (!y_in_place && overlaps(a->y, yb, a->x, xb)) || overlaps(a->residual_out, ob, a->x, xb) ||
+      overlaps(a->residual_out, ob, a->gate, gb) || overlaps(a->residual_out, ob, a->w_post, wb) ||
+      overlaps(a->residual_out, ob, a->w_pre, wb) ||
+      (!res_in_place && overlaps(a->residual_out, ob, a->residual, ib)))
+    return GDR_ERR_ALIAS;
+  p.x = static_cast<const uint16_t *>(a->x);
+  p.w_post = a->w_post;
+  p.gate = static_cast<const uint16_t *>(a->gate);
+  p.res = a->residual;
+  p.out = a->residual_out;
+  p.w_pre = a->w_pre;
+  p.y = static_cast<uint16_t *>(a->y);
+  p.post = a->post_norm;
+  p.res_fp32 = a->residual_fp32;
+  p.alpha = a->alpha;
+  p.eps_post = a->eps_post;
+  p.eps_pre = a->eps_pre;
+  return launch_block_norm(p, rows, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -89,6 +89,55 @@ int launch_chunk_prefill(const void *q, const void *k, const void *v, int64_t qk
                          float eps, void *y, void *workspace, size_t ws_bytes, cudaStream_t s,
                          const PrefillPool *pool = nullptr);
 size_t chunk_prefill_workspace_bytes(int n_seqs, int hv, int window_chunks, bool need_carry);
+// Decayed linear attention: where a sequence's state comes from and goes to.  Dense arrays
+// (h0 and / or hT, either may be null), or a pool addressed by slot[n] (slot set; a slot
+// outside [0, n_slots) starts from zero and keeps nothing).
+struct DecayStates {
+  const float *h0;
+  float *hT;
+  const int32_t *slot;
+  float *pool;
+  int n_slots;
+  int init_from_pool;
+#ifdef __CUDACC__
+  __device__ __forceinline__ void resolve(int n, int h, int hv, const float **in, float **out) const {
+    constexpr int64_t kState = static_cast<int64_t>(kHeadDim) * kHeadDim;
+    if (slot) {
+      const int64_t e = slot[n];
+      float *s = e >= 0 && e < n_slots ? pool + (e * hv + h) * kState : nullptr;
+      *in = init_from_pool ? s : nullptr;
+      *out = s;
+    } else {
+      const int64_t at = (static_cast<int64_t>(n) * hv + h) * kState;
+      *in = h0 ? h0 + at : nullptr;
+      *out = hT ? hT + at : nullptr;
+    }
+  }
+#endif
+};
+int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, const float *log_decay, float scale, int hk, int hv,
+                         const int32_t *cu_dev, const int32_t *cu_host, int n_seqs, const DecayStates &states,
+                         void *o, void *workspace, cudaStream_t s);
+// bytes of workspace a prefill of these sequences runs on (0: none)
+size_t decay_prefill_workspace_bytes(const int32_t *cu_host, int n_seqs, int hv);
+int launch_decay_decode(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const float *log_decay, float scale, int hk, int hv, float *state,
+                        const int32_t *slot, int n_slots, void *o, int batch, cudaStream_t s);
+// gdr_block_norm with strides in elements and every default filled in (block_norm.cu)
+struct BlockNormParams {
+  const uint16_t *x;
+  const float *w_post;
+  const uint16_t *gate;
+  const void *res;
+  void *out;
+  const float *w_pre;
+  uint16_t *y;
+  int64_t x_stride, gate_stride, res_stride, out_stride, y_stride;
+  int d, post, res_fp32;
+  float alpha, eps_post, eps_pre;
+};
+int launch_block_norm(const BlockNormParams &p, int64_t rows, cudaStream_t s);
 // y[M][N] = x[M][K] W[N][K]^T in bf16 with fp32 accumulation (linear.cu)
 int launch_linear(const void *x, const void *w, void *y, int64_t M, int64_t N, int64_t K, cudaStream_t s);
 // window schedule of a prefill call on the current device (windows, chunks per window,

@@ -396,6 +396,133 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
                       void *y, void *stream);
 
 /*
+ * Decayed linear attention -- a recurrent attention layer without the delta
+ * term, beside the gated delta rule and on the same states (no counterpart in
+ * the pages: the sibling recurrence with one fixed decay for each head).
+ * Per sequence and value head h, with l = exp(log_decay[h]) and H the [dk][dv]
+ * fp32 state:
+ *     H_t = l H_{t-1} + k_t v_t^T
+ *     o_t = scale * H_t^T q_t
+ * q and k are used as they are (no norm); value head h reads key head
+ * h / (hv / hk).  The layouts are those of the calls above: a pool of states can
+ * hold either kind.
+ *   q, k:      bf16 [T][hk][128] rows, consecutive tokens q_stride / k_stride
+ *              elements apart (0 = dense, hk*128)
+ *   v:         bf16 [T][hv][128] rows, v_stride elements apart (0 = dense)
+ *              A stride is at least a row and a multiple of 8, so q, k, v may be
+ *              views of one packed projection.
+ *   log_decay: fp32 [hv]; 0 forgets nothing, -inf everything but the token
+ *              itself; a value above 0 grows the state (as the formula says)
+ *   o:         bf16 [T][hv][128], dense; must not overlap an input or a state
+ *              (GDR_ERR_ALIAS)
+ * Precision: sums and states in fp32.  In the chunked form of the prefill the
+ * probabilities (q.k) l^(i-j) and the state that a chunk's queries read are rounded to
+ * bf16 for the tensor cores (as o itself is); the state that is carried and returned is
+ * not.  A value that is not finite makes its sequence's later outputs and its state not
+ * finite; earlier tokens' outputs and other sequences keep theirs.
+ */
+
+/*
+ * gdr_decay_attn_prefill -- the recurrence over packed sequences.
+ *   cu_seqlens_dev / cu_seqlens_host: [n_seqs + 1] int32, same values.  Rows of o
+ *             behind the last sequence are left as they were.
+ *   h0:       fp32 [n_seqs][hv][128][128] initial state, or NULL = zeros
+ *   hT:       fp32 [n_seqs][hv][128][128] final state, or NULL; may equal h0 (in
+ *             place), must not overlap it otherwise (GDR_ERR_ALIAS).  An empty
+ *             sequence copies its initial state.
+ *   workspace, workspace_bytes: device scratch, 16-byte aligned, at least
+ *             gdr_decay_attn_prefill_workspace_size(...) bytes
+ *             (GDR_ERR_WORKSPACE otherwise; NULL when that is 0).  Its contents
+ *             need no initialisation and are meaningless after the call; two
+ *             calls in flight at the same time must not share it.
+ * Capturable into a CUDA graph (every launch is on `stream`).
+ */
+GDR_API int gdr_decay_attn_prefill(const void *q, const void *k, const void *v, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, const float *log_decay, float scale,
+                                   int hk, int hv, const int32_t *cu_seqlens_dev,
+                                   const int32_t *cu_seqlens_host, int n_seqs, const float *h0, float *hT,
+                                   void *o, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of workspace a prefill of these sequences needs: 0 unless sequences are
+ * split into segments that run beside each other (few heads and sequences for the
+ * GPU), whose states it then holds.  Host only.  0 for invalid arguments.
+ */
+GDR_API size_t gdr_decay_attn_prefill_workspace_size(const int32_t *cu_seqlens_host, int n_seqs, int hv);
+
+/*
+ * gdr_decay_attn_prefill_slots -- the same on a pool of cached states.  Sequence n
+ * starts from entry slot[n] of state_pool (init_from_pool = 1) or from zero (0) and
+ * leaves its final state there; the slot rules are gdr_chunk_prefill_slots': an int32
+ * array in device memory read by the kernels, a slot outside [0, n_slots) starts from
+ * zero and keeps no state, an empty sequence leaves its entry (1) or zeroes it (0), two
+ * sequences naming one entry race.
+ */
+GDR_API int gdr_decay_attn_prefill_slots(const void *q, const void *k, const void *v, int64_t q_stride,
+                                         int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                         float scale, int hk, int hv, const int32_t *cu_seqlens_dev,
+                                         const int32_t *cu_seqlens_host, int n_seqs, float *state_pool,
+                                         int n_slots, const int32_t *slot, int init_from_pool, void *o,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdr_decay_attn_decode -- one token for each of `batch` sequences (at most 65535).
+ *   q, k, v, strides: as above with one row for each sequence
+ *   state: fp32 [batch][hv][128][128], in/out (updated in place)
+ *   o:     bf16 [batch][hv][128]
+ */
+GDR_API int gdr_decay_attn_decode(const void *q, const void *k, const void *v, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, const float *log_decay, float scale,
+                                  int hk, int hv, float *state, void *o, int batch, void *stream);
+
+/*
+ * gdr_decay_attn_decode_slots -- the same on a pool: row i reads and writes entry
+ * slot[i] of state_pool.  The slot rules are gdr_decode_step_slots': a slot outside
+ * [0, n_slots) is a padding row (zero o, the pool is not touched), two rows naming one
+ * entry race.  A row gives the bits of gdr_decay_attn_decode on the same state.
+ */
+GDR_API int gdr_decay_attn_decode_slots(const void *q, const void *k, const void *v, int64_t q_stride,
+                                        int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                        float scale, int hk, int hv, float *state_pool, int n_slots,
+                                        const int32_t *slot, void *o, int batch, void *stream);
+
+/*
+ * gdr_block_norm -- the norms after and before a block with its gate and residual
+ * (no counterpart in the pages: what stands between two layers' kernels).
+ * Per row of d values, in fp32:
+ *     u = post_norm ? x / sqrt(mean(x^2) + eps_post) * w_post : x
+ *     r = residual + alpha * gate * u              -> residual_out
+ *     y = r / sqrt(mean(r^2) + eps_pre) * w_pre    -> y, from the unrounded r
+ * x is the output of the block before, y the input of the next one.
+ * d is a multiple of 8, at most 32768 (GDR_ERR_UNSUPPORTED above).
+ * Strides are between rows, in elements, 0 = dense (d), else at least d and a multiple
+ * of 8.  In place: residual_out may equal residual and y may equal x, with equal
+ * strides; the outputs overlap nothing else (GDR_ERR_ALIAS).
+ */
+typedef struct gdr_block_norm {
+  const void *x;               /* bf16 [rows][d] output of the block */
+  int64_t x_stride;
+  int post_norm;               /* 1: norm x first */
+  const float *w_post;         /* fp32 [d] or NULL (ones); only with post_norm */
+  float eps_post;
+  const void *gate;            /* bf16 [rows][d], or [d] with gate_shared, or NULL (ones) */
+  int64_t gate_stride;         /* not read with gate_shared */
+  int gate_shared;             /* 1: one gate row [d] for all rows */
+  float alpha;                 /* scale of the block's contribution */
+  const void *residual;        /* [rows][d], bf16 or fp32, or NULL (zeros) */
+  int64_t residual_stride;
+  int residual_fp32;           /* 1: residual and residual_out are fp32 */
+  void *residual_out;          /* [rows][d] in residual's type, or NULL (not needed) */
+  int64_t residual_out_stride;
+  const float *w_pre;          /* fp32 [d] or NULL (ones); only with y */
+  float eps_pre;
+  void *y;                     /* bf16 [rows][d], or NULL (no norm before a next block) */
+  int64_t y_stride;
+} gdr_block_norm_t;
+
+GDR_API int gdr_block_norm(const gdr_block_norm_t *args, int64_t rows, int64_t d, void *stream);
+
+/*
  * Text of the last host-side failure of a call made from this thread: which
  * step failed and the CUDA error string (empty when the last call succeeded).
  * The pointer stays valid until the next call from the same thread.

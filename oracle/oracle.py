@@ -341,3 +341,38 @@ def decode_step_slots(x, a, b, conv_w, A_log, dt_bias, conv_pool, state_pool, sl
     cpool[ids] = cs
     spool[ids] = Hn
     return o_bits, cpool, spool
+
+
+# ---------------------------------------------------------------------------
+# decayed linear attention and the norms around a block (fp64, numpy)
+# ---------------------------------------------------------------------------
+
+def decay_attn(q, k, v, log_decay, cu, h0=None, scale=1.0):
+    """H_t = exp(log_decay) H_{t-1} + k_t v_t^T, o_t = scale H_t^T q_t, token by token in fp64.
+
+    q, k [T, hk, d], v [T, hv, d], log_decay [hv], cu [N + 1], h0 [N, hv, d, d] or None (zeros);
+    value head h reads key head h // (hv / hk).  Returns (o [T, hv, d], final states)."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    lam = np.exp(np.asarray(log_decay, dtype=np.float64))[:, None, None]
+    n, hv, d = len(cu) - 1, v.shape[1], v.shape[2]
+    key = np.arange(hv) // (hv // q.shape[1])
+    o = np.zeros((v.shape[0], hv, d))
+    H = np.zeros((n, hv, d, d)) if h0 is None else np.array(h0, dtype=np.float64)
+    for i in range(n):
+        for t in range(int(cu[i]), int(cu[i + 1])):
+            H[i] = lam * H[i] + k[t, key][:, :, None] * v[t][:, None, :]
+            o[t] = scale * np.einsum("hi,hij->hj", q[t, key], H[i])
+    return o, H
+
+
+def block_norm(x, residual=None, gate=None, post_norm=False, w_post=None, w_pre=None, alpha=1.0, eps_post=1e-6,
+               eps_pre=1e-6):
+    """u = x / rms(x) * w_post (or x), r = residual + alpha gate u, y = r / rms(r) * w_pre in fp64."""
+    u = np.asarray(x, dtype=np.float64)
+    if post_norm:
+        u = u / np.sqrt(np.mean(u * u, axis=-1, keepdims=True) + eps_post)
+        u = u if w_post is None else u * np.asarray(w_post, dtype=np.float64)
+    u = alpha * (u if gate is None else u * np.asarray(gate, dtype=np.float64))
+    r = u if residual is None else np.asarray(residual, dtype=np.float64) + u
+    y = r / np.sqrt(np.mean(r * r, axis=-1, keepdims=True) + eps_pre)
+    return r, (y if w_pre is None else y * np.asarray(w_pre, dtype=np.float64))
