@@ -3,41 +3,47 @@
 // Per sequence and value head, with l = exp(log_decay[h]) and H the [dk][dv] fp32 state:
 //     H_t = l H_{t-1} + k_t v_t^T,   o_t = scale * H_t^T q_t
 // In chunks of 64 tokens (local index i, H0 the state before the chunk):
-//     o_i = scale * (l^{i+1} H0^T q_i + sum_{j<=i} P_ij v_j),  P_ij = l^{i-j} (q_i . k_j)
-//     H   = l^64 H0 + sum_j k_j v'_j^T,                        v'_j = l^{63-j} v_j
+//     o_i = scale l^{i+1} H0^T q_i + sum_{j<=i} P_ij v_j,   P_ij = scale l^{i-j} (q_i . k_j)
+//     H   = l^64 H0 + sum_j k_j v'_j^T,                     v'_j = l^{63-j} v_j
 // l is one number for a head, so every decay factor of a chunk is a constant of the CTA, and
 // what a chunk adds to the state does not depend on the state: the only chain from chunk to
 // chunk is one multiply-add on H.
 //
-// The products, everything transposed so that M = 128 rows are used wherever they can be:
+// The products, transposed so that M = 128 rows are used wherever they can be:
 //     S   = Q K^T                 M = 64 (tokens),  N = 64,  K = 128
 //     KV  = V'^T K                M = 128 (dv),     N = 128, K = 64;  V' in three bf16 terms
 //     OI  = H0^T Q^T              M = 128 (dv),     N = 64,  K = 128; H0 in two bf16 terms
 //     PV  = V^T P^T               M = 128 (dv),     N = 64,  K = 64;  P in two bf16 terms
 // q, k, v are bf16 and exact.  H0 and P (fp32) as hi + lo bf16 keep 16 bits of them, an error
 // far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the state stays an
-// fp32 sum (with two terms its error was to be 2.7e-6, ten times that of fp32 sums).
+// fp32 sum (two terms would leave it an error of about 2.7e-6, ten times that of fp32 sums).
+//
+// What bounds a chunk is shared memory: MMA operands, copies and the tiles that are written
+// for them.  V' and H0 are therefore A operands in tensor memory, written from registers.
 //
 // One CTA (14 warps) walks the chunks of one (value head, sequence or segment of one):
 //   warps 0..3   P from S (TMEM -> registers -> shared memory), and o from OI and PV
-//   warps 4..11  V' (shared memory -> TMEM, the A operand of KV), the state H in registers
-//                (thread = one dv row, 64 of its dk columns), H's bf16 terms for OI
-//   warp 12      TMA of the Q, K, V tiles into a ring of three stages
-//   warp 13      every product, in the order KV(c), OI(c), PV(c), S(c + 1): each one's inputs
-//                are made while the ones before it run
+//   warps 4..11  V' (shared memory -> TMEM), the state H in registers (thread = one dv row,
+//                64 of its dk columns), H's bf16 terms (-> TMEM)
+//   warp 12      TMA of the Q, K, V tiles into a ring of four stages
+//   warp 13      every product, in the order KV(c) lo and mid terms, S(c), KV(c) hi terms,
+//                OI(c), PV(c): what each one needs is made while the ones before it run
 // The handoffs are mbarriers (what completes it -> what it allows):
-//   full[s]      the copies of a chunk landed -> S and KV may read them, V' may be made
+//   full[s]      the copies of a chunk landed -> the products may read them, V' may be made
 //   empty[s]     the chunk's last product is done -> its stage may be refilled
-//   vt[c & 1]    V' of chunk c is in TMEM (and a partial chunk's tail rows are zero) -> KV(c)
-//   kv           KV(c) is done -> the state takes it
+//   vt[]         V' of chunk c is in TMEM (and a partial chunk's tail rows are zero) -> KV(c), S(c)
+//   kv           KV(c) is done -> the state takes it, V' may be rewritten
 //   kv_free      the state has read KV(c) -> KV(c + 1) may overwrite it
-//   h            H before chunk c is in shared memory -> OI(c)
-//   oi           OI(c) is done -> H's tiles may be rewritten
-//   s            S(c) is done, and with it all of chunk c - 1 -> P(c) and o(c - 1)
-//   p            P(c) is in shared memory and S(c) read -> PV(c), S(c + 1)
-//   o_free       o(c) is out of TMEM -> OI(c + 1)
-// No barrier runs two phases ahead of a waiter: each arrival for chunk c + 1 (c + 2 for vt)
-// comes after a wait on something that was issued behind the wait for chunk c.
+//   s            S(c) is done -> P(c)
+//   s_read       S(c) is in registers -> OI(c), which takes its columns
+//   h            H before chunk c is in TMEM -> OI(c)
+//   oi           OI(c) is done -> H may be rewritten
+//   p            P(c) is in shared memory -> PV(c)
+//   o            PV(c) is done, and with it all of chunk c -> o(c), P may be rewritten
+//   o_free       o(c) is out of TMEM -> S(c + 1), PV(c + 1)
+// No barrier runs two phases ahead of a waiter: each arrival for chunk c + 1 comes after a
+// wait on something that was issued behind the wait for chunk c (vt has two barriers in the
+// state-only launch, where V' has two buffers, and the same holds for c + 2).
 //
 // Few heads and sequences leave SMs idle, so long sequences are then cut into segments that
 // run beside each other: a first launch (kOut = false: K and V only) leaves what each segment
@@ -60,24 +66,24 @@ namespace {
 constexpr int D = kHeadDim;
 constexpr int C = kChunk;            // tokens of a chunk
 constexpr int kThreads = 448;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kSms = 148;
 
 constexpr uint32_t HALF = C * 128;                  // [64 tokens][64 columns] bf16
 constexpr uint32_t TILE = 2 * HALF;                 // [64 tokens][128] bf16
 constexpr uint32_t STAGE = 3 * TILE;                // K, V, Q
 constexpr uint32_t OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE;
-constexpr uint32_t H_HALF = D * 128;                // [128 dv][64 dk] bf16
-constexpr uint32_t OFF_H = kStages * STAGE;         // hi (dk halves 0, 1), lo (0, 1)
-constexpr uint32_t OFF_P = OFF_H + 4 * H_HALF;      // hi, lo: [64 i][64 j] bf16
-constexpr uint32_t OFF_TAB = OFF_P + 2 * HALF;      // l^{63-j} [64], scale l^{i+1} [64]
-constexpr uint32_t OFF_BAD = OFF_TAB + 2 * C * 4;   // [4 chunks][2 token halves][128 dv] bytes
+constexpr uint32_t OFF_P = kStages * STAGE;         // hi, lo: [64 i][64 j] bf16
+constexpr uint32_t OFF_O = OFF_P + 2 * HALF;        // 4 warps x [64 tokens][32 dv] bf16
+constexpr uint32_t O_TILE = C * 64;
+constexpr uint32_t OFF_BAD = OFF_O + 4 * O_TILE;    // [4 chunks][2 token halves][128 dv] bytes
 constexpr uint32_t OFF_BAR = OFF_BAD + 4 * 2 * D;
 constexpr uint32_t kSmem = OFF_BAR + 192 + 1024;    // + alignment of the tiles
 static_assert(kSmem <= 232448, "decay prefill shared memory exceeds 227 KB");
 
-// TMEM columns
-constexpr uint32_t TC_KV = 0, TC_VT = 128, TC_S = 320, TC_OI = 384, TC_PV = 448, TC_ALL = 512;
+// TMEM columns.  S and OI share theirs; the state-only launch has no H, S, OI and PV and keeps
+// two V' buffers.
+constexpr uint32_t TC_KV = 0, TC_H = 128, TC_VT = 256, TC_S = 352, TC_OI = TC_S, TC_PV = 416, TC_ALL = 512;
 constexpr uint32_t VT_TERM = C / 2, VT_BUF = 3 * VT_TERM;
 
 struct DecayPrefillParams {
@@ -103,24 +109,92 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 16 columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+// 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 16 lanes x 16 columns: thread t holds, for each block n of 4 columns, lane t / 4 (r[2n]) and
+// lane 8 + t / 4 (r[2n + 1]) of column 4 n + t % 4
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 lanes x 32 columns: thread t gets, for each block n of 8 columns, columns 8 n + 2 (t % 4) and
+// the next one of lane t / 4 (v[4n], v[4n + 1]) and of lane 8 + t / 4 (v[4n + 2], v[4n + 3])
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float *v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 lanes x 64 columns: thread t < 16 gets lane t, columns 0..31; thread t >= 16 lane t - 16,
+// columns 32..63
+__device__ __forceinline__ void tmem_ld32x2(uint32_t taddr, float *v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// (hi, lo) halves of a packed bf16 pair as floats
-__device__ __forceinline__ float pair_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float pair_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// four 8 x 8 tiles of 16-bit values, transposed on the way: thread t gets, of each, the values of
+// memory rows 2 (t % 4) and the next one in memory column t / 4
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, const uint32_t *r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void *tmap, int32_t x, int32_t y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
+// The top 16 bits of two floats, packed (the first one low).
+__device__ __forceinline__ uint32_t tops(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&b);
 }
+// What is left of two floats behind their top 16 bits (a bf16 value, cut off): exact.
+__device__ __forceinline__ float2 behind_tops(float2 x) {
+  const float2 t = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFF0000u),
+                               __uint_as_float(__float_as_uint(x.y) & 0xFFFF0000u));
+  return __ffma2_rn(t, make_float2(-1.0f, -1.0f), x);
+}
+
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
@@ -170,7 +244,8 @@ __device__ __forceinline__ Unit find_unit(const int32_t *cu, int n_seqs, int seg
 template <bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DecayPrefillParams p) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                     const __grid_constant__ DecayPrefillParams p) {
   grid_dep_wait();
   grid_dep_launch();
   const int h = blockIdx.x, unit = blockIdx.y;
@@ -194,14 +269,11 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (sbase - raw_addr);
-  float *tab_d = reinterpret_cast<float *>(smem + OFF_TAB);
-  float *tab_r = tab_d + C;
   volatile uint8_t *bad = smem + OFF_BAD;
-  const uint32_t bars = sbase + OFF_BAR;
-  const uint32_t b_full = bars, b_empty = bars + 8 * kStages, b_vt = b_empty + 8 * kStages;
-  const uint32_t b_kv = b_vt + 16, b_kv_free = b_kv + 8, b_h = b_kv + 16, b_oi = b_kv + 24, b_s = b_kv + 32,
-                 b_p = b_kv + 40, b_o_free = b_kv + 48, b_drain = b_kv + 56;
-  constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 8);
+  const uint32_t b_full = sbase + OFF_BAR, b_empty = b_full + 8 * kStages, b_vt = b_empty + 8 * kStages;
+  const uint32_t b_kv = b_vt + 16, b_kv_free = b_kv + 8, b_s = b_kv + 16, b_s_read = b_kv + 24, b_h = b_kv + 32,
+                 b_oi = b_kv + 40, b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
+  constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 10);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + OFF_BAR + kWords);
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + OFF_BAR + kWords + 4);
   static_assert(kWords + 8 <= 192, "barrier block");
@@ -215,21 +287,22 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(b_vt + 8, 8);
     mbar_init(b_kv, 1);
     mbar_init(b_kv_free, 8);
+    mbar_init(b_s, 1);
+    mbar_init(b_s_read, 4);
     mbar_init(b_h, 8);
     mbar_init(b_oi, 1);
-    mbar_init(b_s, 1);
     mbar_init(b_p, 4);
+    mbar_init(b_o, 1);
     mbar_init(b_o_free, 4);
     mbar_init(b_drain, 1);
     *abort_flag = 0u;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    if (kOut) tma_prefetch_desc(&tm_q);
-  }
-  if (tid < C) {
-    tab_d[tid] = decay_pow(g, C - 1 - tid);
-    tab_r[tid] = p.scale * decay_pow(g, tid + 1);
+    if (kOut) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_o);
+    }
   }
   for (int i = tid; i < 4 * 2 * D; i += kThreads) bad[i] = 0xFF;
   if (warp == 13) {
@@ -240,15 +313,22 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  const auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
+  // the same for all lanes of a warp: they go on, or give up, together
+  const auto wait_warp = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+  // V' buffer and barrier of chunk c, and the barrier's phase
+  const auto vt_col = [&](int c) { return tmem + (kOut ? TC_VT : TC_H + (c & 1) * VT_BUF); };
+  const auto wait_vt = [&](int c) { return kOut ? wait(b_vt, c) : wait(b_vt + 8 * (c & 1), c >> 1); };
+  const auto vt_bar = [&](int c) { return kOut ? b_vt : b_vt + 8 * (c & 1); };
 
   if (warp == 12) {
     if (lane == 0) {
-      // ---- copies: chunk c into stage c % 3 once the products of chunk c - 3 are done
+      // ---- copies: chunk c into a stage once the products of the chunk before it there are done
       const int qk_col = (h / p.group) * D, v_col = h * D;
       int issued = 0;
       for (int c = 0; c < n_chunks; ++c) {
         const int s = c % kStages;
-        if (c >= kStages && !chain_wait(b_empty + 8 * s, ((c / kStages) - 1) & 1, abort_flag, p.err)) break;
+        if (c >= kStages && !wait(b_empty + 8 * s, (c / kStages) - 1)) break;
         const uint32_t st = sbase + s * STAGE, full = b_full + 8 * s;
         const int t0 = t_begin + c * C;
         mbar_arrive_expect_tx(full, kOut ? STAGE : 2 * TILE);
@@ -270,197 +350,195 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   } else if (warp == 13) {
     if (lane == 0) {
       // ---- products
-      const int last_len = t_end - t_begin - (n_chunks - 1) * C;
-      auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
-      auto issue_s = [&](int c) {
-        const int s = c % kStages;
-        if (!wait(b_full + 8 * s, c / kStages)) return false;
-        // a partial chunk: after the rows behind its end are zeroed
-        if (c == n_chunks - 1 && last_len < C && !wait(b_vt + 8 * (c & 1), c >> 1)) return false;
-        tc_fence_after();
-        const uint32_t st = sbase + s * STAGE;
-        const uint32_t id = idesc_bf16(64, 64, false, false);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-          mma_bf16(tmem + TC_S, sdesc(st + OFF_Q + off, 16, 1024), sdesc(st + OFF_K + off, 16, 1024), id, kk > 0);
-        }
-        return true;
-      };
-      bool go = true;
-      if (kOut && n_chunks > 0) {
-        go = issue_s(0);
-        if (go) mma_commit(b_s);
-      }
-      for (int c = 0; c < n_chunks && go; ++c) {
+      for (int c = 0; c < n_chunks; ++c) {
         const int s = c % kStages;
         const uint32_t st = sbase + s * STAGE;
-        // KV(c) = V'^T K
-        if (!wait(b_full + 8 * s, c / kStages) || !wait(b_vt + 8 * (c & 1), c >> 1) ||
-            (c > 0 && !wait(b_kv_free, c - 1)))
-          break;
+        if (!wait(b_full + 8 * s, c / kStages) || !wait_vt(c) || (c > 0 && !wait(b_kv_free, c - 1))) break;
         tc_fence_after();
-        {
-          const uint32_t id = idesc_bf16(128, 128, false, true);
-          const uint32_t vt = tmem + TC_VT + (c & 1) * VT_BUF;
-          const uint64_t bk = sdesc(st + OFF_K, HALF, 1024);
+        const uint64_t bk = sdesc(st + OFF_K, HALF, 1024);
+        const auto issue_kv = [&](int term) {
 #pragma unroll
-          for (int term = 2; term >= 0; --term)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + TC_KV, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), id,
-                          term < 2 || kk > 0);
-          mma_commit(b_kv);
-        }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(tmem + TC_KV, vt_col(c) + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4),
+                        idesc_bf16(128, 128, false, true), term < 2 || kk > 0);
+        };
+        issue_kv(2);
+        issue_kv(1);
         if (!kOut) {
+          issue_kv(0);
+          mma_commit(b_kv);
           mma_commit(b_empty + 8 * s);
           continue;
         }
-        // OI(c) = H0^T Q^T
-        if (!wait(b_h, c) || (c > 0 && !wait(b_o_free, c - 1))) break;
+        // S(c) = Q K^T
+        if (c > 0 && !wait(b_o_free, c - 1)) break;
         tc_fence_after();
-        {
-          const uint32_t id = idesc_bf16(128, 64, false, false);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16(tmem + TC_OI,
-                       sdesc(sbase + OFF_H + (2 * part + (kk >> 2)) * H_HALF + (kk & 3) * 32, 16, 1024),
-                       sdesc(st + OFF_Q + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024), id, (part | kk) != 0);
-          mma_commit(b_oi);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
+          mma_bf16(tmem + TC_S, sdesc(st + OFF_Q + off, 16, 1024), sdesc(st + OFF_K + off, 16, 1024),
+                   idesc_bf16(64, 64, false, false), kk > 0);
         }
+        mma_commit(b_s);
+        issue_kv(0);
+        mma_commit(b_kv);
+        // OI(c) = H0^T Q^T
+        if (!wait(b_h, c) || !wait(b_s_read, c)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8,
+                        sdesc(st + OFF_Q + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024),
+                        idesc_bf16(128, 64, false, false), part < 1 || kk > 0);
+        mma_commit(b_oi);
         // PV(c) = V^T P^T
         if (!wait(b_p, c)) break;
         tc_fence_after();
-        {
-          const uint32_t id = idesc_bf16(128, 64, true, false);
-          const uint64_t av = sdesc(st + OFF_V, HALF, 1024);
+        const uint64_t av = sdesc(st + OFF_V, HALF, 1024);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+        for (int part = 1; part >= 0; --part)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), sdesc(sbase + OFF_P + part * HALF + kk * 32, 16, 1024),
-                       id, (part | kk) != 0);
-          mma_commit(b_empty + 8 * s);
-        }
-        if (c + 1 < n_chunks) go = issue_s(c + 1);
-        if (go) mma_commit(b_s);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), sdesc(sbase + OFF_P + part * HALF + kk * 32, 16, 1024),
+                     idesc_bf16(128, 64, true, false), part < 1 || kk > 0);
+        mma_commit(b_o);
+        mma_commit(b_empty + 8 * s);
       }
       mma_commit(b_drain);   // every product issued is complete before tensor memory is released
       mbar_wait(b_drain, 0, p.err, 1u << 20);
     }
     __syncwarp();
   } else if (warp < 4) {
-    if (kOut && n_chunks > 0) {
-      // ---- P(c) and o(c - 1)
+    if (kOut) {
+      // ---- P(c) and o(c)
       // S as an M = 64 product: rows 16 w .. 16 w + 15 in lanes 32 w .. 32 w + 15; thread t takes row
       // 16 w + (t & 15), columns 32 (t >> 4) .. + 31.  Its 32 decay factors and its part of the
       // causal mask (as masks of packed pairs) are the same in every chunk.
       const int i = 16 * warp + (lane & 15), j0 = 32 * (lane >> 4);
-      float f[32];
+      float2 f[16];
       uint32_t keep[16];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] = i >= j0 + e ? decay_pow(g, i - j0 - e) : 0.0f;
+      for (int e = 0; e < 16; ++e) {
+        const int j = j0 + 2 * e;
+        f[e].x = i >= j ? p.scale * decay_pow(g, i - j) : 0.0f;
+        f[e].y = i >= j + 1 ? p.scale * decay_pow(g, i - j - 1) : 0.0f;
+        keep[e] = (i >= j ? 0x0000FFFFu : 0u) | (i >= j + 1 ? 0xFFFF0000u : 0u);
+      }
+      // o: thread t holds tokens 8 n + 2 (t % 4) and the next one of dv rows t / 4 + 8 b + 16 gr
+      float2 r[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        keep[e] = (i >= j0 + 2 * e ? 0x0000FFFFu : 0u) | (i >= j0 + 2 * e + 1 ? 0xFFFF0000u : 0u);
+      for (int n = 0; n < 8; ++n) {
+        const int tok = 8 * n + 2 * (lane & 3);
+        r[n] = make_float2(p.scale * decay_pow(g, tok + 1), p.scale * decay_pow(g, tok + 2));
+      }
       const uint32_t quarter = static_cast<uint32_t>(32 * warp) << 16;
-      const int dv = 32 * warp + lane;
-      const int64_t o_step = static_cast<int64_t>(p.hv) * D;
-      for (int c = 0; c <= n_chunks; ++c) {
-        if (!chain_wait(b_s, c & 1, abort_flag, p.err)) break;
-        __syncwarp();
+      const uint32_t otile = sbase + OFF_O + warp * O_TILE;
+      // this lane's row address in the transposed 8 x 8 stores: token 8 (m >> 1) + (lane & 7) of a pair
+      // of token blocks, dv block m & 1, m = lane >> 3 (64-byte rows, 16-byte chunk ^ (row / 2) % 4)
+      const uint32_t otok = 8 * (lane >> 4) + (lane & 7);
+      const uint32_t orow = otile + otok * 64, oswz = (otok >> 1) & 3, ochunk = (lane >> 3) & 1;
+      for (int c = 0; c < n_chunks; ++c) {
+        if (!wait_warp(b_s, c)) break;
         tc_fence_after();
-        uint32_t out[32];   // o(c - 1) of this thread's dv, two tokens a word
-        int first_bad = C;
-        if (c > 0) {
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            float oi[32], pv[32];
-            tmem_ld32(tmem + quarter + TC_OI + 32 * part, oi);
-            tmem_ld32(tmem + quarter + TC_PV + 32 * part, pv);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 r = *reinterpret_cast<const float4 *>(tab_r + 32 * part + e);
-              out[16 * part + e / 2] = pack_pair(fmaf(oi[e], r.x, p.scale * pv[e]), fmaf(oi[e + 1], r.y, p.scale * pv[e + 1]));
-              out[16 * part + e / 2 + 1] =
-                  pack_pair(fmaf(oi[e + 2], r.z, p.scale * pv[e + 2]), fmaf(oi[e + 3], r.w, p.scale * pv[e + 3]));
-            }
-          }
-          volatile uint8_t *b0 = bad + ((c - 1) & 3) * 2 * D + dv;
-          const int x0 = b0[0], x1 = b0[D];
-          first_bad = min(min(x0, x1), C);
-          if (first_bad < C) b0[0] = b0[D] = 0xFF;
+        {
+          float sv[32];
+          tmem_ld32x2(tmem + quarter + TC_S, sv);
+          tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_o_free);
-        }
-        if (c < n_chunks) {
-          float sv[32];
-          {
-            uint32_t r[32];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
-                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;\n"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                  "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                  "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                  "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                  "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                : "r"(tmem + quarter + TC_S));
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(r[e]) * f[e];
-          }
+          if (lane == 0) mbar_arrive(b_s_read);
 #pragma unroll
           for (int v8 = 0; v8 < 4; ++v8) {
-            uint4 hi, lo;
-            split8x2(sv + 8 * v8, hi, lo);
-            const uint32_t *m = keep + 4 * v8;
-            hi = make_uint4(hi.x & m[0], hi.y & m[1], hi.z & m[2], hi.w & m[3]);
-            lo = make_uint4(lo.x & m[0], lo.y & m[1], lo.z & m[2], lo.w & m[3]);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = 4 * v8 + e;
+              const float2 x = __fmul2_rn(make_float2(sv[2 * at], sv[2 * at + 1]), f[at]);
+              const float2 y = behind_tops(x);
+              hi[e] = tops(x.x, x.y) & keep[at];
+              lo[e] = pack_pair(y.x, y.y) & keep[at];
+            }
             const uint32_t at = sbase + OFF_P + sw128(i, (j0 >> 3) + v8);
-            st_shared16(at, hi);
-            st_shared16(at + HALF, lo);
+            st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_shared16(at + HALF, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
-          fence_proxy_async();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_p);
         }
-        if (c > 0) {
-          const int t0 = t_begin + (c - 1) * C, len = min(C, t_end - t0);
-          uint16_t *dst = p.o + (static_cast<int64_t>(t0) * p.hv + h) * D + dv;
-          if (first_bad < C) {   // a value that is not finite reached every later row of this dv
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_p);
+          if (c > 0) bulk_wait_read();   // o(c - 1) has left its tile
+        }
+        if (!wait_warp(b_o, c)) break;
+        tc_fence_after();
+        // a value that was not finite reaches every later row of its dv (see warps 4..11)
+        volatile uint8_t *mark = bad + (c & 3) * 2 * D + 32 * warp + lane;
+        const int x0 = mark[0], x1 = mark[D];
+        const int first_bad = min(x0, x1);
+        const bool any_bad = __any_sync(0xffffffffu, first_bad != 0xFF);
+        if (first_bad != 0xFF) mark[0] = mark[D] = 0xFF;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              out[e] |= (first_bad <= 2 * e ? 0x7FFFu : 0u) | (first_bad <= 2 * e + 1 ? 0x7FFF0000u : 0u);
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            float oi[16], pv[16];
+            const uint32_t at = tmem + quarter + (static_cast<uint32_t>(16 * gr) << 16) + 32 * part;
+            tmem_ld_16x256b_x4(at + TC_OI, oi);
+            tmem_ld_16x256b_x4(at + TC_PV, pv);
+            tmem_wait_ld();
+            uint32_t w[8];   // [token block n][dv block b]
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int e = 4 * n + 2 * b;
+                const float2 x = __ffma2_rn(make_float2(oi[e], oi[e + 1]), r[4 * part + n], make_float2(pv[e], pv[e + 1]));
+                w[2 * n + b] = pack_pair(x.x, x.y);
+              }
+            if (any_bad) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int from = __shfl_sync(0xffffffffu, first_bad, 16 * gr + 8 * b + (lane >> 2));
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  const int tok = 32 * part + 8 * n + 2 * (lane & 3);
+                  w[2 * n + b] |= (from <= tok ? 0x7FFFu : 0u) | (from <= tok + 1 ? 0x7FFF0000u : 0u);
+                }
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; n += 2)
+              stsm_x4_t(orow + (32 * part + 8 * n) * 64 + (((2 * gr + ochunk) ^ oswz) << 4), w + 2 * n);
           }
-          if (len == C) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              dst[(2 * e) * o_step] = static_cast<uint16_t>(out[e]);
-              dst[(2 * e + 1) * o_step] = static_cast<uint16_t>(out[e] >> 16);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (2 * e < len) dst[(2 * e) * o_step] = static_cast<uint16_t>(out[e]);
-              if (2 * e + 1 < len) dst[(2 * e + 1) * o_step] = static_cast<uint16_t>(out[e] >> 16);
-            }
+        tc_fence_before();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_o_free);
+        const int t0 = t_begin + c * C, len = min(C, t_end - t0);
+        if (len == C) {
+          if (lane == 0) {
+            tma_store_2d(&tm_o, h * D + 32 * warp, t0, otile);
+            bulk_commit();
+          }
+        } else {   // the rows behind the end belong to others
+          for (int x = lane; x < 4 * len; x += 32) {
+            const int tok = x >> 2;
+            const uint4 v = ld_shared16(otile + tok * 64 + (((x & 3) ^ ((tok >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(t0 + tok) * p.hv + h) * D + 32 * warp + 8 * (x & 3)) = v;
           }
         }
       }
+      if (lane == 0) bulk_wait_all();
+      __syncwarp();
     }
   } else {
     // ---- the state: thread = row dv of H^T, dk columns 64 half .. + 63; V' of tokens 32 half .. + 31
     const int half = (warp - 4) >> 2, q4 = warp & 3;
     const int dv = 32 * q4 + lane;
     const uint32_t quarter = static_cast<uint32_t>(32 * q4) << 16;
-    float H[64];
+    float2 H[32];
     {
       const int64_t at = static_cast<int64_t>(64 * half) * D + dv;
       if (un.seg == 0) {
@@ -469,158 +547,165 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                            : (kOut && un.segs > 1) ? ws + (un.segs - 1) * ws_step
                                                    : state_in;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) H[e] = src ? src[at + e * D] : 0.0f;
+        for (int e = 0; e < 32; ++e)
+          H[e] = src ? make_float2(src[at + 2 * e * D], src[at + (2 * e + 1) * D]) : make_float2(0.0f, 0.0f);
         if (!kOut && src) {
-          float *copy = ws + (un.segs - 1) * ws_step;
+          float *copy = ws + (un.segs - 1) * ws_step + at;
 #pragma unroll
-          for (int e = 0; e < 64; ++e) copy[at + e * D] = H[e];
+          for (int e = 0; e < 32; ++e) {
+            copy[2 * e * D] = H[e].x;
+            copy[(2 * e + 1) * D] = H[e].y;
+          }
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) H[e] = 0.0f;
+        for (int e = 0; e < 32; ++e) H[e] = make_float2(0.0f, 0.0f);
         if (kOut) {   // the segments before this one, each decayed over those after it
-          const DecayStep seg_step = decay_step(g, static_cast<int64_t>(p.seg_chunks) * C);
+          const DecayStep step = decay_step(g, static_cast<int64_t>(p.seg_chunks) * C);
           for (int j = 0; j < un.seg; ++j) {
             const float *src = ws + j * ws_step + at;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) H[e] = seg_step.apply(H[e], src[e * D]);
+            for (int e = 0; e < 32; ++e)
+              H[e] = step.apply2(H[e], make_float2(src[2 * e * D], src[(2 * e + 1) * D]));
           }
         }
       }
     }
-    const DecayStep full_step = decay_step(g, C);
-    // this thread's column of a [64 tokens][128] tile: 16-byte chunk (dv >> 3) & 7 of half dv >> 6
-    uint32_t col[8];
+    // V': this warp's 32 dv x 32 tokens as transposed 8 x 8 tiles.  Lane l gives the address of row
+    // l & 7 of tile l >> 3: token block (l >> 4), dv block (l >> 3) & 1; thread t holds tokens
+    // 32 half + 8 n + 2 (t % 4) and the next one of dv rows t / 4 + 8 b + 16 gr.
+    const uint32_t vrow = (q4 >> 1) * HALF + (32 * half + 8 * (lane >> 4) + (lane & 7)) * 128;
+    const uint32_t vchunk = 4 * (q4 & 1) + ((lane >> 3) & 1);
+    const int tok0 = 32 * half + 2 * (lane & 3);
+    float2 d[4];
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      col[r] = (dv >> 6) * HALF + (32 * half + r) * 128 + ((((dv >> 3) & 7) ^ r) << 4) + (dv & 7) * 2;
-    bool go = true;
-    for (int c = 0; c < n_chunks; ++c) {
-      const int s = c % kStages;
-      const uint32_t st = sbase + s * STAGE;
+    for (int n = 0; n < 4; ++n)
+      d[n] = make_float2(decay_pow(g, C - 1 - (tok0 + 8 * n)), decay_pow(g, C - 2 - (tok0 + 8 * n)));
+    // byte offset of (row 32 half + r, column dv) in a [64 tokens][128] tile
+    const auto elem = [&](int r) {
+      return (dv >> 6) * HALF + (32 * half + r) * 128 + ((((dv >> 3) & 7) ^ (r & 7)) << 4) + (dv & 7) * 2;
+    };
+    const DecayStep full_step = decay_step(g, C), last_step = decay_step(g, t_end - t_begin - (n_chunks - 1) * C);
+    const auto make_vt = [&](int c) {
+      const uint32_t st = sbase + (c % kStages) * STAGE;
       const int len = min(C, t_end - t_begin - c * C);
-      go = chain_wait(b_full + 8 * s, (c / kStages) & 1, abort_flag, p.err);
-      if (!go) break;
-      __syncwarp();
-      // V'(c): its buffer is free, KV(c - 2) being done
-      const uint32_t vbase = st + OFF_V;
-      float nf = 0.0f;   // NaN once a value was not finite
-      if (len < C) {     // rows behind the end: zero in K and V, so that nothing there is multiplied
+      if (len < C) {   // rows behind the end: zero in K and V, so that nothing there is multiplied
 #pragma unroll 1
         for (int r = 0; r < 32; ++r)
           if (32 * half + r >= len) {
-            const uint32_t at = st + col[0] - ((((dv >> 3) & 7)) << 4) + r * 128 + ((((dv >> 3) & 7) ^ (r & 7)) << 4);
-            st_shared_u16(at + OFF_V, 0);
-            st_shared_u16(at + OFF_K, 0);
+            st_shared_u16(st + OFF_V + elem(r), 0);
+            st_shared_u16(st + OFF_K + elem(r), 0);
           }
-      }
-      {
-        uint32_t t0[16], t1[16], t2[16];
-        const uint32_t tab = sbase + OFF_TAB + 4 * (32 * half);
+        __syncwarp();
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          const int r = 2 * m;
-          const float v0 = __uint_as_float(ld_shared_u16(vbase + col[r & 7] + (r >> 3) * 1024) << 16);
-          const float v1 = __uint_as_float(ld_shared_u16(vbase + col[(r + 1) & 7] + (r >> 3) * 1024) << 16);
-          nf = fmaf(v0, 0.0f, nf);
-          nf = fmaf(v1, 0.0f, nf);
-          float d0, d1;
-          if (len == C) {
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];\n" : "=f"(d0), "=f"(d1) : "r"(tab + 4 * r));
-          } else {   // l^{len-1-j}; the rows behind the end hold zeros
-            const int j = 32 * half + r + C - len;
-            d0 = tab_d[min(j, C - 1)];
-            d1 = tab_d[min(j + 1, C - 1)];
-          }
-          const float p0 = d0 * v0, p1 = d1 * v1;
-          t0[m] = pack_pair(p0, p1);
-          const float r0 = p0 - pair_lo(t0[m]), r1 = p1 - pair_hi(t0[m]);
-          t1[m] = pack_pair(r0, r1);
-          t2[m] = pack_pair(r0 - pair_lo(t1[m]), r1 - pair_hi(t1[m]));
+        for (int n = 0; n < 4; ++n) {   // (the last chunk: the others' factors are not needed any more)
+          const int left = len - 1 - (tok0 + 8 * n);
+          d[n] = make_float2(left >= 0 ? decay_pow(g, left) : 0.0f, left >= 1 ? decay_pow(g, left - 1) : 0.0f);
         }
-        const uint32_t vt = tmem + quarter + TC_VT + (c & 1) * VT_BUF + 16 * half;
-        tmem_st16(vt, t0);
-        tmem_st16(vt + VT_TERM, t1);
-        tmem_st16(vt + 2 * VT_TERM, t2);
       }
-      if (kOut && nf != nf) {
+      float2 nf = make_float2(0.0f, 0.0f);   // NaN once a value was not finite
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        uint32_t raw[8], hi[8], mid[8], lo[8];
+        const uint32_t at = st + OFF_V + vrow + (((vchunk + 2 * gr) ^ (lane & 7)) << 4);
+        ldsm_x4_t(at, raw);
+        ldsm_x4_t(at + 16 * 128, raw + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {   // e = 2 n + b
+          const float2 v = make_float2(__uint_as_float(raw[e] << 16), __uint_as_float(raw[e] & 0xFFFF0000u));
+          if (kOut) nf = __ffma2_rn(v, make_float2(0.0f, 0.0f), nf);
+          const float2 x = __fmul2_rn(v, d[e >> 1]);
+          const float2 y = behind_tops(x);
+          const float2 z = behind_tops(y);
+          hi[e] = tops(x.x, x.y);
+          mid[e] = tops(y.x, y.y);
+          lo[e] = pack_pair(z.x, z.y);
+        }
+        const uint32_t vt = vt_col(c) + quarter + (static_cast<uint32_t>(16 * gr) << 16) + 16 * half;
+        tmem_st_16x128b_x4(vt, hi);
+        tmem_st_16x128b_x4(vt + VT_TERM, mid);
+        tmem_st_16x128b_x4(vt + 2 * VT_TERM, lo);
+      }
+      bool wrote = len < C;
+      if (kOut && __any_sync(0xffffffffu, nf.x != nf.x || nf.y != nf.y)) {
         // PV multiplies every value of the chunk, by zero where it is still to come: take what is not
         // finite out of the tile and tell warps 0..3 from which token on this dv is not finite
         int first = 0xFF;
 #pragma unroll 1
         for (int r = 31; r >= 0; --r) {
-          const uint32_t at = vbase + (dv >> 6) * HALF + (32 * half + r) * 128 + ((((dv >> 3) & 7) ^ (r & 7)) << 4) +
-                              (dv & 7) * 2;
+          const uint32_t at = st + OFF_V + elem(r);
           if ((ld_shared_u16(at) & 0x7F80u) == 0x7F80u) {
             st_shared_u16(at, 0);
             first = 32 * half + r;
           }
         }
         bad[(c & 3) * 2 * D + half * D + dv] = static_cast<uint8_t>(first);
+        wrote = true;
       }
-      if (len < C || nf != nf) fence_proxy_async();
+      if (wrote) fence_proxy_async();
       __syncwarp();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_vt + 8 * (c & 1));
-      if (c > 0) {   // H before chunk c
-        go = chain_wait(b_kv, (c - 1) & 1, abort_flag, p.err);
-        if (!go) break;
-        __syncwarp();
-        tc_fence_after();
+      if (lane == 0) mbar_arrive(vt_bar(c));
+    };
+    const auto take_kv = [&](int c) {   // H <- l^n H + KV(c)
+      if (!wait_warp(b_kv, c)) return false;
+      tc_fence_after();
+      const DecayStep now = c < n_chunks - 1 ? full_step : last_step;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          float kv[32];
-          tmem_ld32(tmem + quarter + TC_KV + 64 * half + 32 * part, kv);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) H[32 * part + e] = full_step.apply(H[32 * part + e], kv[e]);
+      for (int part = 0; part < 2; ++part) {
+        float kv[32];
+        tmem_ld32(tmem + quarter + TC_KV + 64 * half + 32 * part, kv);
+        tmem_wait_ld();
+        if (part == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_kv_free);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          H[16 * part + e] = now.apply2(H[16 * part + e], make_float2(kv[2 * e], kv[2 * e + 1]));
+      }
+      return true;
+    };
+    bool go = true;
+    for (int c = 0; c < n_chunks; ++c) {
+      go = wait_warp(b_full + 8 * (c % kStages), c / kStages);
+      if (!go) break;
+      make_vt(c);
+      if (kOut) {
+        // H before chunk c, once OI(c - 1) has read the one before
+        if (c > 0 && !(go = wait_warp(b_oi, c - 1))) break;
+        tc_fence_after();
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = tops(H[e].x, H[e].y);
+        tmem_st32(tmem + quarter + TC_H + 32 * half, w);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 y = behind_tops(H[e]);
+          w[e] = pack_pair(y.x, y.y);
+        }
+        tmem_st32(tmem + quarter + TC_H + 64 + 32 * half, w);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_kv_free);
-      }
-      if (kOut) {
-        if (c > 0) {
-          go = chain_wait(b_oi, (c - 1) & 1, abort_flag, p.err);
-          if (!go) break;
-          __syncwarp();
-        }
-#pragma unroll
-        for (int v8 = 0; v8 < 8; ++v8) {
-          uint4 hi, lo;
-          split8x2(H + 8 * v8, hi, lo);
-          const uint32_t at = sbase + OFF_H + half * H_HALF + sw128(dv, v8);
-          st_shared16(at, hi);
-          st_shared16(at + 2 * H_HALF, lo);
-        }
-        fence_proxy_async();
-        __syncwarp();
         if (lane == 0) mbar_arrive(b_h);
+        if (!(go = take_kv(c))) break;
+      } else if (c > 0) {
+        if (!(go = take_kv(c - 1))) break;
       }
     }
-    if (go && n_chunks > 0) {
-      go = chain_wait(b_kv, (n_chunks - 1) & 1, abort_flag, p.err);
-      __syncwarp();
-      if (go) {
-        tc_fence_after();
-        const DecayStep step = decay_step(g, t_end - t_begin - (n_chunks - 1) * C);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          float kv[32];
-          tmem_ld32(tmem + quarter + TC_KV + 64 * half + 32 * part, kv);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) H[32 * part + e] = step.apply(H[32 * part + e], kv[e]);
-        }
-      }
-    }
+    if (!kOut && go) go = take_kv(n_chunks - 1);
     float *dst = !kOut ? ws + un.seg * ws_step : un.seg == un.segs - 1 ? state_out : nullptr;
     if (go && dst) {
       dst += static_cast<int64_t>(64 * half) * D + dv;
 #pragma unroll
-      for (int e = 0; e < 64; ++e) dst[e * D] = H[e];
+      for (int e = 0; e < 32; ++e) {
+        dst[2 * e * D] = H[e].x;
+        dst[(2 * e + 1) * D] = H[e].y;
+      }
     }
   }
   tc_fence_before();
@@ -677,14 +762,15 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
   return best;
 }
 
-bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride) {
+bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride, uint32_t box_cols,
+              CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {row_stride * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(C)};
+  const cuuint32_t box[2] = {box_cols, static_cast<cuuint32_t>(C)};
   const cuuint32_t estr[2] = {1, 1};
   return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -714,15 +800,16 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
     return launch_status(cudaErrorSymbolNotFound, "decay prefill: cuTensorMapEncodeTiled lookup");
   const DecayPlan plan = plan_decay(cu_host, n_seqs, hv);
   if (plan.units > 65535) return GDR_ERR_SHAPE;
-  CUtensorMap tq, tk, tv;
-  // without a token nothing is copied; the maps still need a valid address
+  // without a token nothing is copied; the maps still need an address
   const bool any = cu_host[n_seqs] > 0;
-  const void *qb = any ? q : cu_dev, *kb = any ? k : cu_dev, *vb = any ? v : cu_dev;
-  if (!any) qb = kb = vb = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(cu_dev) & ~uintptr_t{15});
+  const void *none = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(cu_dev) & ~uintptr_t{15});
   const uint64_t rows = any ? static_cast<uint64_t>(cu_host[n_seqs]) : 1;
-  if (!make_map(&tq, qb, static_cast<uint64_t>(hk) * D, rows, static_cast<uint64_t>(q_stride)) ||
-      !make_map(&tk, kb, static_cast<uint64_t>(hk) * D, rows, static_cast<uint64_t>(k_stride)) ||
-      !make_map(&tv, vb, static_cast<uint64_t>(hv) * D, rows, static_cast<uint64_t>(v_stride)))
+  const uint64_t qk_cols = static_cast<uint64_t>(hk) * D, v_cols = static_cast<uint64_t>(hv) * D;
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map(&tq, any ? q : none, qk_cols, rows, static_cast<uint64_t>(q_stride), 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tk, any ? k : none, qk_cols, rows, static_cast<uint64_t>(k_stride), 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tv, any ? v : none, v_cols, rows, static_cast<uint64_t>(v_stride), 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&to, any ? o : none, v_cols, rows, v_cols, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return launch_status(cudaErrorInvalidValue, "decay prefill: tensor map encoding");
   DecayPrefillParams p;
   p.cu = cu_dev;
@@ -738,11 +825,11 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   p.err = device_error_ptr();
   const dim3 grid(hv, plan.units);
   if (plan.seg_chunks != 0) {
-    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, p),
+    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
                                  "decay prefill: segment kernel launch");
     if (st) return st;
   }
-  return launch_status(launch_pdl(decay_prefill_kernel<true>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, p),
+  return launch_status(launch_pdl(decay_prefill_kernel<true>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
                        "decay prefill: kernel launch");
 }
 

@@ -17,6 +17,9 @@ __device__ __forceinline__ float decay_pow(float g, int64_t n) {
 struct DecayStep {
   float a, b;
   __device__ __forceinline__ float apply(float H, float add) const { return fmaf(a, H, fmaf(b, H, add)); }
+  __device__ __forceinline__ float2 apply2(float2 H, float2 add) const {
+    return __ffma2_rn(make_float2(a, a), H, __ffma2_rn(make_float2(b, b), H, add));
+  }
 };
 __device__ __forceinline__ DecayStep decay_step(float g, int64_t n) {
   const float x = n == 0 ? 0.0f : g * static_cast<float>(n);
