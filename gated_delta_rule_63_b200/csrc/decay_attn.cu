@@ -26,24 +26,27 @@
 //   warps 4..11  V' (shared memory -> TMEM), the state H in registers (thread = one dv row,
 //                64 of its dk columns), H's bf16 terms (-> TMEM)
 //   warp 12      TMA of the Q, K, V tiles into a ring of four stages
-//   warp 13      every product, in the order KV(c) lo and mid terms, S(c), KV(c) hi terms,
-//                OI(c), PV(c): what each one needs is made while the ones before it run
+//   warp 13      every product, in the order KV(c), S(c), OI(c), PV(c): what each one needs is
+//                made while the ones before it run.  The warp stays together and one elected
+//                lane issues, so that descriptors are made in uniform registers: issued from
+//                a branch of lane 0 each product took 76 to 117 cycles of issuing alone.
 // The handoffs are mbarriers (what completes it -> what it allows):
 //   full[s]      the copies of a chunk landed -> the products may read them, V' may be made
 //   empty[s]     the chunk's last product is done -> its stage may be refilled
-//   vt[]         V' of chunk c is in TMEM (and a partial chunk's tail rows are zero) -> KV(c), S(c)
-//   kv           KV(c) is done -> the state takes it, V' may be rewritten
-//   kv_free      the state has read KV(c) -> KV(c + 1) may overwrite it
-//   s            S(c) is done -> P(c)
-//   s_read       S(c) is in registers -> OI(c), which takes its columns
+//   vt[]         V' of chunk c is in TMEM, KV(c - 1) has been read, a partial chunk's tail rows
+//                are zero -> KV(c), S(c)
+//   kv[]         KV(c) is done -> the state takes it
+//   s            S(c) is done (and KV(c)) -> P(c)
+//   s_read       S(c) is in registers -> V'(c + 1), whose columns it shares
 //   h            H before chunk c is in TMEM -> OI(c)
 //   oi           OI(c) is done -> H may be rewritten
 //   p            P(c) is in shared memory -> PV(c)
 //   o            PV(c) is done, and with it all of chunk c -> o(c), P may be rewritten
-//   o_free       o(c) is out of TMEM -> S(c + 1), PV(c + 1)
+//   o_free       o(c) is out of TMEM -> OI(c + 1), PV(c + 1)
+// (Products execute in the order of their issue, so S(c) may take V's columns behind KV(c).)
 // No barrier runs two phases ahead of a waiter: each arrival for chunk c + 1 comes after a
-// wait on something that was issued behind the wait for chunk c (vt has two barriers in the
-// state-only launch, where V' has two buffers, and the same holds for c + 2).
+// wait on something that was issued behind the wait for chunk c.  In the state-only launch V'
+// and KV have two buffers and vt and kv two barriers each, and the same holds for c + 2.
 //
 // Few heads and sequences leave SMs idle, so long sequences are then cut into segments that
 // run beside each other: a first launch (kOut = false: K and V only) leaves what each segment
@@ -81,9 +84,10 @@ constexpr uint32_t OFF_BAR = OFF_BAD + 4 * 2 * D;
 constexpr uint32_t kSmem = OFF_BAR + 192 + 1024;    // + alignment of the tiles
 static_assert(kSmem <= 232448, "decay prefill shared memory exceeds 227 KB");
 
-// TMEM columns.  S and OI share theirs; the state-only launch has no H, S, OI and PV and keeps
-// two V' buffers.
-constexpr uint32_t TC_KV = 0, TC_H = 128, TC_VT = 256, TC_S = 352, TC_OI = TC_S, TC_PV = 416, TC_ALL = 512;
+// TMEM columns.  S takes V's columns once KV is done with them; the state-only launch has no H,
+// S, OI and PV and keeps two buffers of V' and of KV.
+constexpr uint32_t TC_KV = 0, TC_H = 128, TC_VT = 256, TC_S = TC_VT, TC_OI = 352, TC_PV = 416, TC_ALL = 512;
+constexpr uint32_t TC_VT2 = 128, TC_KV2 = 320;
 constexpr uint32_t VT_TERM = C / 2, VT_BUF = 3 * VT_TERM;
 
 struct DecayPrefillParams {
@@ -107,6 +111,13 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// true in one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
 }
 
 // 32 columns of this thread's TMEM lane
@@ -271,8 +282,8 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint8_t *smem = smem_raw + (sbase - raw_addr);
   volatile uint8_t *bad = smem + OFF_BAD;
   const uint32_t b_full = sbase + OFF_BAR, b_empty = b_full + 8 * kStages, b_vt = b_empty + 8 * kStages;
-  const uint32_t b_kv = b_vt + 16, b_kv_free = b_kv + 8, b_s = b_kv + 16, b_s_read = b_kv + 24, b_h = b_kv + 32,
-                 b_oi = b_kv + 40, b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
+  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_s_read = b_kv + 24, b_h = b_kv + 32, b_oi = b_kv + 40,
+                 b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
   constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 10);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + OFF_BAR + kWords);
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + OFF_BAR + kWords + 4);
@@ -286,7 +297,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(b_vt, 8);
     mbar_init(b_vt + 8, 8);
     mbar_init(b_kv, 1);
-    mbar_init(b_kv_free, 8);
+    mbar_init(b_kv + 8, 1);
     mbar_init(b_s, 1);
     mbar_init(b_s_read, 4);
     mbar_init(b_h, 8);
@@ -316,10 +327,12 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
   // the same for all lanes of a warp: they go on, or give up, together
   const auto wait_warp = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-  // V' buffer and barrier of chunk c, and the barrier's phase
-  const auto vt_col = [&](int c) { return tmem + (kOut ? TC_VT : TC_H + (c & 1) * VT_BUF); };
-  const auto wait_vt = [&](int c) { return kOut ? wait(b_vt, c) : wait(b_vt + 8 * (c & 1), c >> 1); };
+  // V' and KV of chunk c: their columns, barriers and the barriers' phase
+  const auto vt_col = [&](int c) { return tmem + (kOut ? TC_VT : TC_VT2 + (c & 1) * VT_BUF); };
+  const auto kv_col = [&](int c) { return tmem + (kOut || (c & 1) == 0 ? TC_KV : TC_KV2); };
   const auto vt_bar = [&](int c) { return kOut ? b_vt : b_vt + 8 * (c & 1); };
+  const auto kv_bar = [&](int c) { return kOut ? b_kv : b_kv + 8 * (c & 1); };
+  const auto phase2 = [&](int c) { return kOut ? c : c >> 1; };
 
   if (warp == 12) {
     if (lane == 0) {
@@ -348,64 +361,73 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     __syncwarp();
   } else if (warp == 13) {
-    if (lane == 0) {
-      // ---- products
-      for (int c = 0; c < n_chunks; ++c) {
-        const int s = c % kStages;
-        const uint32_t st = sbase + s * STAGE;
-        if (!wait(b_full + 8 * s, c / kStages) || !wait_vt(c) || (c > 0 && !wait(b_kv_free, c - 1))) break;
-        tc_fence_after();
-        const uint64_t bk = sdesc(st + OFF_K, HALF, 1024);
-        const auto issue_kv = [&](int term) {
+    // ---- products
+    const bool elected = elect_one();
+    // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
+    const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
+    const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
+    const uint64_t dp = sdesc(sbase + OFF_P, 16, 1024);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int s = c % kStages;
+      const uint64_t st = static_cast<uint64_t>(s * STAGE) >> 4;
+      if (!wait_warp(b_full + 8 * s, c / kStages) || !wait_warp(vt_bar(c), phase2(c))) break;
+      tc_fence_after();
+      const uint32_t kv = kv_col(c), vt = vt_col(c);
+      const uint64_t bk = dk_mn0 + st, aq = dq0 + st;
+      if (elected) {
+        // KV(c) = V'^T K, the smallest terms first
+#pragma unroll
+        for (int term = 2; term >= 0; --term)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ts(tmem + TC_KV, vt_col(c) + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4),
-                        idesc_bf16(128, 128, false, true), term < 2 || kk > 0);
-        };
-        issue_kv(2);
-        issue_kv(1);
-        if (!kOut) {
-          issue_kv(0);
-          mma_commit(b_kv);
-          mma_commit(b_empty + 8 * s);
-          continue;
-        }
+            mma_bf16_ts(kv, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), idesc_bf16(128, 128, false, true),
+                        term < 2 || kk > 0);
+        mma_commit(kv_bar(c));
+        if (!kOut) mma_commit(b_empty + 8 * s);
+      }
+      __syncwarp();
+      if (!kOut) continue;
+      if (elected) {
         // S(c) = Q K^T
-        if (c > 0 && !wait(b_o_free, c - 1)) break;
-        tc_fence_after();
+        const uint64_t bks = dk0 + st;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-          mma_bf16(tmem + TC_S, sdesc(st + OFF_Q + off, 16, 1024), sdesc(st + OFF_K + off, 16, 1024),
-                   idesc_bf16(64, 64, false, false), kk > 0);
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          mma_bf16(tmem + TC_S, aq + off, bks + off, idesc_bf16(64, 64, false, false), kk > 0);
         }
         mma_commit(b_s);
-        issue_kv(0);
-        mma_commit(b_kv);
+      }
+      __syncwarp();
+      if (!wait_warp(b_h, c) || (c > 0 && !wait_warp(b_o_free, c - 1))) break;
+      tc_fence_after();
+      if (elected) {
         // OI(c) = H0^T Q^T
-        if (!wait(b_h, c) || !wait(b_s_read, c)) break;
-        tc_fence_after();
 #pragma unroll
         for (int part = 1; part >= 0; --part)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8,
-                        sdesc(st + OFF_Q + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024),
+            mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8, aq + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
                         idesc_bf16(128, 64, false, false), part < 1 || kk > 0);
         mma_commit(b_oi);
+      }
+      __syncwarp();
+      if (!wait_warp(b_p, c)) break;
+      tc_fence_after();
+      if (elected) {
         // PV(c) = V^T P^T
-        if (!wait(b_p, c)) break;
-        tc_fence_after();
-        const uint64_t av = sdesc(st + OFF_V, HALF, 1024);
+        const uint64_t av = dv_mn0 + st;
 #pragma unroll
         for (int part = 1; part >= 0; --part)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), sdesc(sbase + OFF_P + part * HALF + kk * 32, 16, 1024),
+            mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), dp + ((part * HALF + kk * 32) >> 4),
                      idesc_bf16(128, 64, true, false), part < 1 || kk > 0);
         mma_commit(b_o);
         mma_commit(b_empty + 8 * s);
       }
+      __syncwarp();
+    }
+    if (elected) {
       mma_commit(b_drain);   // every product issued is complete before tensor memory is released
       mbar_wait(b_drain, 0, p.err, 1u << 20);
     }
@@ -497,25 +519,20 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const float2 x = __ffma2_rn(make_float2(oi[e], oi[e + 1]), r[4 * part + n], make_float2(pv[e], pv[e + 1]));
                 w[2 * n + b] = pack_pair(x.x, x.y);
               }
-            if (any_bad) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int from = __shfl_sync(0xffffffffu, first_bad, 16 * gr + 8 * b + (lane >> 2));
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                  const int tok = 32 * part + 8 * n + 2 * (lane & 3);
-                  w[2 * n + b] |= (from <= tok ? 0x7FFFu : 0u) | (from <= tok + 1 ? 0x7FFF0000u : 0u);
-                }
-              }
-            }
 #pragma unroll
             for (int n = 0; n < 4; n += 2)
               stsm_x4_t(orow + (32 * part + 8 * n) * 64 + (((2 * gr + ochunk) ^ oswz) << 4), w + 2 * n);
           }
         tc_fence_before();
-        fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_o_free);
+        if (any_bad) {
+#pragma unroll 1
+          for (int tok = first_bad; tok < C; ++tok)
+            st_shared_u16(otile + tok * 64 + (((lane >> 3) ^ ((tok >> 1) & 3)) << 4) + (lane & 7) * 2, 0x7FFF);
+        }
+        fence_proxy_async();
+        __syncwarp();
         const int t0 = t_begin + c * C, len = min(C, t_end - t0);
         if (len == C) {
           if (lane == 0) {
@@ -650,19 +667,14 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (lane == 0) mbar_arrive(vt_bar(c));
     };
     const auto take_kv = [&](int c) {   // H <- l^n H + KV(c)
-      if (!wait_warp(b_kv, c)) return false;
+      if (!wait_warp(kv_bar(c), phase2(c))) return false;
       tc_fence_after();
       const DecayStep now = c < n_chunks - 1 ? full_step : last_step;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         float kv[32];
-        tmem_ld32(tmem + quarter + TC_KV + 64 * half + 32 * part, kv);
+        tmem_ld32(kv_col(c) + quarter + 64 * half + 32 * part, kv);
         tmem_wait_ld();
-        if (part == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_kv_free);
-        }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           H[16 * part + e] = now.apply2(H[16 * part + e], make_float2(kv[2 * e], kv[2 * e + 1]));
@@ -671,8 +683,9 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     };
     bool go = true;
     for (int c = 0; c < n_chunks; ++c) {
-      go = wait_warp(b_full + 8 * (c % kStages), c / kStages);
+      go = wait_warp(b_full + 8 * (c % kStages), c / kStages) && (!kOut || c == 0 || wait_warp(b_s_read, c - 1));
       if (!go) break;
+      tc_fence_after();
       make_vt(c);
       if (kOut) {
         // H before chunk c, once OI(c - 1) has read the one before
