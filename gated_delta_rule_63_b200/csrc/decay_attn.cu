@@ -33,17 +33,16 @@
 // The handoffs are mbarriers (what completes it -> what it allows):
 //   full[s]      the copies of a chunk landed -> the products may read them, V' may be made
 //   empty[s]     the chunk's last product is done -> its stage may be refilled
-//   vt[]         V' of chunk c is in TMEM, KV(c - 1) has been read, a partial chunk's tail rows
-//                are zero -> KV(c), S(c)
-//   kv[]         KV(c) is done -> the state takes it
-//   s            S(c) is done (and KV(c)) -> P(c)
-//   s_read       S(c) is in registers -> V'(c + 1), whose columns it shares
+//   vt[]         V' of chunk c is in TMEM, a partial chunk's tail rows are zero -> KV(c), S(c)
+//   kv[]         KV(c) is done -> the state takes it, V' may be rewritten
+//   kv_free      the state has read KV(c) -> KV(c + 1) may overwrite it
+//   s            S(c) is done -> P(c)
 //   h            H before chunk c is in TMEM -> OI(c)
 //   oi           OI(c) is done -> H may be rewritten
 //   p            P(c) is in shared memory -> PV(c)
 //   o            PV(c) is done, and with it all of chunk c -> o(c), P may be rewritten
-//   o_free       o(c) is out of TMEM -> OI(c + 1), PV(c + 1)
-// (Products execute in the order of their issue, so S(c) may take V's columns behind KV(c).)
+//   o_free       o(c) is out of TMEM -> S(c + 1), OI(c + 1)
+// S and PV share their columns: P(c), which PV(c) waits for, is made from S(c).
 // No barrier runs two phases ahead of a waiter: each arrival for chunk c + 1 comes after a
 // wait on something that was issued behind the wait for chunk c.  In the state-only launch V'
 // and KV have two buffers and vt and kv two barriers each, and the same holds for c + 2.
@@ -68,7 +67,10 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int C = kChunk;            // tokens of a chunk
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
+// registers a thread: 128 at launch (512 x 128 is the whole file); warps 12..15 give up theirs for
+// the state's: 128 x 56 + 128 x 128 + 256 x 160 = 64512 of 65536
+constexpr int kRegsFew = 56, kRegsState = 168, kRegsOut = 120;
 constexpr int kStages = 4;
 constexpr int kSms = 148;
 
@@ -84,22 +86,30 @@ constexpr uint32_t OFF_BAR = OFF_BAD + 4 * 2 * D;
 constexpr uint32_t kSmem = OFF_BAR + 192 + 1024;    // + alignment of the tiles
 static_assert(kSmem <= 232448, "decay prefill shared memory exceeds 227 KB");
 
-// TMEM columns.  S takes V's columns once KV is done with them; the state-only launch has no H,
-// S, OI and PV and keeps two buffers of V' and of KV.
-constexpr uint32_t TC_KV = 0, TC_H = 128, TC_VT = 256, TC_S = TC_VT, TC_OI = 352, TC_PV = 416, TC_ALL = 512;
+// TMEM columns.  S and PV share theirs; the state-only launch has no H, S, OI and PV and keeps two
+// buffers of V' and of KV.
+constexpr uint32_t TC_KV = 0, TC_H = 128, TC_VT = 256, TC_OI = 352, TC_PV = 416, TC_S = TC_PV, TC_ALL = 512;
 constexpr uint32_t TC_VT2 = 128, TC_KV2 = 320;
 constexpr uint32_t VT_TERM = C / 2, VT_BUF = 3 * VT_TERM;
 
+constexpr int kListed = 64;    // sequences whose offsets ride in the launch parameters
+constexpr int kMostSplit = 32; // sequences of a call that may be split into segments
+
 struct DecayPrefillParams {
-  const int32_t *cu;
+  const int32_t *cu;   // offsets in device memory, read when there are more than kListed sequences
   const float *log_decay;
   float scale;
   int hv, group, n_seqs;
   int seg_chunks;      // chunks of a segment; 0: every sequence is one unit
   DecayStates st;
-  float *ws;           // [units][hv][D][D]: what segments add; a sequence's last: its initial state
+  float *ws;           // [segments][hv][D][D]: what segments add; a sequence's last: its initial state
   uint16_t *o;
   int *err;
+  // Up to kListed sequences: where each begins and ends, the longest first (a launch then ends with
+  // short ones, and no global load precedes the first copy), and which it is in the call.
+  int32_t begin[kListed], end[kListed];
+  uint8_t seq[kListed];
+  int16_t first[kMostSplit];   // with segments: number of the sequence's first one
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]
@@ -112,6 +122,11 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs)); }
 
 // true in one lane of the warp
 __device__ __forceinline__ bool elect_one() {
@@ -137,6 +152,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
 __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// ... and x 8 columns
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 // 16 lanes x 32 columns: thread t gets, for each block n of 8 columns, columns 8 n + 2 (t % 4) and
@@ -189,7 +210,6 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, int32_t x, int32_
                "r"(x), "r"(y), "r"(src)
                : "memory");
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
 // The top 16 bits of two floats, packed (the first one low).
 __device__ __forceinline__ uint32_t tops(float a, float b) {
@@ -206,6 +226,59 @@ __device__ __forceinline__ float2 behind_tops(float2 x) {
   return __ffma2_rn(t, make_float2(-1.0f, -1.0f), x);
 }
 
+// One warp's part of V'^T: its 32 dv rows (lane quarter q4) of 16 NB tokens from tok_base on, as three
+// bf16 terms of d_j v_j.  V is read from its [tokens][dv] tile as transposed 8 x 8 tiles: lane l gives
+// the address of row l & 7 of tile l >> 3 (token block l >> 4, dv block (l >> 3) & 1), and thread t
+// gets tokens 8 n + 2 (t % 4) and the next one of dv rows t / 4 + 8 b of a group of 16.
+template <int NB>
+struct VPart {
+  uint32_t row, chunk;   // of the lane's address in a V tile
+  uint32_t place;        // TMEM lanes and first column
+  int tok0;              // the thread's first token
+  float2 d[2 * NB];      // the decay factors of its tokens
+  __device__ __forceinline__ VPart(float g, int lane, int q4, int tok_base) {
+    row = (q4 >> 1) * HALF + (tok_base + 8 * (lane >> 4) + (lane & 7)) * 128;
+    chunk = 4 * (q4 & 1) + ((lane >> 3) & 1);
+    place = (static_cast<uint32_t>(32 * q4) << 16) + tok_base / 2;
+    tok0 = tok_base + 2 * (lane & 3);
+    factors(g, C);
+  }
+  __device__ __forceinline__ void factors(float g, int len) {   // l^{len-1-j}, 0 behind the end
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) {
+      const int left = len - 1 - (tok0 + 8 * n);
+      d[n] = make_float2(left >= 0 ? decay_pow(g, left) : 0.0f, left >= 1 ? decay_pow(g, left - 1) : 0.0f);
+    }
+  }
+  // group gr of 16 dv rows: w[4 NB term + 2 n + b]; nf turns NaN where a value is not finite
+  template <bool kCheck>
+  __device__ __forceinline__ void split(uint32_t tile, int gr, int lane, uint32_t *w, float2 &nf) const {
+    uint32_t raw[4 * NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      ldsm_x4_t(tile + row + i * 16 * 128 + (((chunk + 2 * gr) ^ (lane & 7)) << 4), raw + 4 * i);
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+      const float2 v = make_float2(__uint_as_float(raw[e] << 16), __uint_as_float(raw[e] & 0xFFFF0000u));
+      if (kCheck) nf = __ffma2_rn(v, make_float2(0.0f, 0.0f), nf);
+      const float2 x = __fmul2_rn(v, d[e >> 1]);
+      const float2 y = behind_tops(x);
+      const float2 z = behind_tops(y);
+      w[e] = tops(x.x, x.y);
+      w[4 * NB + e] = tops(y.x, y.y);
+      w[8 * NB + e] = pack_pair(z.x, z.y);
+    }
+  }
+  __device__ __forceinline__ void store(uint32_t vt, int gr, const uint32_t *w) const {
+    const uint32_t at = vt + place + (static_cast<uint32_t>(16 * gr) << 16);
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+      if constexpr (NB == 2) tmem_st_16x128b_x4(at + term * VT_TERM, w + 8 * term);
+      else tmem_st_16x128b_x2(at + term * VT_TERM, w + 4 * term);
+    }
+  }
+};
+
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
@@ -215,40 +288,27 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"(v) : "memory");
 }
 
-// Which part of which sequence a unit is.  Segments are counted over the sequences in order
-// (a sequence without tokens is one unit), 32 sequences at a time by the warp.
+// Which part of which sequence a unit is.  Units are the segments of the listed sequences in turn
+// (a sequence without tokens is one), in the state-only launch without each sequence's last.
 struct Unit {
   int seq, seg, segs;
+  int first;          // number of the sequence's first segment
+  int t_begin, t_end;
 };
-__device__ __forceinline__ Unit find_unit(const int32_t *cu, int n_seqs, int seg_chunks, int unit) {
-  Unit u{unit, 0, 1};
-  if (seg_chunks == 0) return u;
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int n0 = 0; n0 < n_seqs; n0 += 32) {
-    const int n = n0 + lane;
-    int segs = 0;
-    if (n < n_seqs) {
-      const int chunks = (cu[n + 1] - cu[n] + C - 1) / C;
-      segs = chunks > 0 ? (chunks + seg_chunks - 1) / seg_chunks : 1;
-    }
-    int upto = segs;   // inclusive sum over the lanes
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += x;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, unit < before + upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      u.seq = n0 + src;
-      u.segs = __shfl_sync(0xffffffffu, segs, src);
-      u.seg = unit - (before + __shfl_sync(0xffffffffu, upto, src) - u.segs);
-      return u;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  u.seq = -1;   // not reached: the host launches as many units as there are
+template <bool kOut>
+__device__ __forceinline__ Unit find_unit(const DecayPrefillParams &p, int unit) {
+  if (p.n_seqs > kListed) return Unit{unit, 0, 1, unit, p.cu[unit], p.cu[unit + 1]};
+  if (p.seg_chunks == 0) return Unit{p.seq[unit], 0, 1, unit, p.begin[unit], p.end[unit]};
+  int i = 0;   // the last one whose first unit is not behind this one
+  while (i + 1 < p.n_seqs && unit >= p.first[i + 1] - (kOut ? 0 : i + 1)) ++i;
+  Unit u;
+  u.seq = p.seq[i];
+  u.first = p.first[i];
+  u.seg = unit - (u.first - (kOut ? 0 : i));
+  const int chunks = (p.end[i] - p.begin[i] + C - 1) / C;
+  u.segs = max(1, (chunks + p.seg_chunks - 1) / p.seg_chunks);
+  u.t_begin = p.begin[i] + u.seg * p.seg_chunks * C;
+  u.t_end = u.seg == u.segs - 1 ? p.end[i] : u.t_begin + p.seg_chunks * C;
   return u;
 }
 
@@ -257,32 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                      const __grid_constant__ DecayPrefillParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int h = blockIdx.x, unit = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Unit un = find_unit(p.cu, p.n_seqs, p.seg_chunks, unit);
-  if (un.seq < 0 || (!kOut && un.seg == un.segs - 1)) return;   // nobody reads what the last segment adds
-  const int s0 = p.cu[un.seq];
-  const int t_begin = s0 + (un.seg > 0 ? un.seg * p.seg_chunks * C : 0);
-  const int t_end = un.seg == un.segs - 1 ? p.cu[un.seq + 1] : t_begin + p.seg_chunks * C;
-  const int n_chunks = (t_end - t_begin + C - 1) / C;
-  const float g = p.log_decay[h];
-  const float *state_in;
-  float *state_out;
-  p.st.resolve(un.seq, h, p.hv, &state_in, &state_out);
-  constexpr int64_t kState = static_cast<int64_t>(D) * D;
-  // this sequence's segments in the workspace are the units unit - seg .. unit - seg + segs - 1
-  float *ws = p.ws + (static_cast<int64_t>(unit - un.seg) * p.hv + h) * kState;
-  const int64_t ws_step = p.hv * kState;
-
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (sbase - raw_addr);
   volatile uint8_t *bad = smem + OFF_BAD;
   const uint32_t b_full = sbase + OFF_BAR, b_empty = b_full + 8 * kStages, b_vt = b_empty + 8 * kStages;
-  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_s_read = b_kv + 24, b_h = b_kv + 32, b_oi = b_kv + 40,
+  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_kv_free = b_kv + 24, b_h = b_kv + 32, b_oi = b_kv + 40,
                  b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
   constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 10);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + OFF_BAR + kWords);
@@ -294,12 +336,12 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(b_full + 8 * s, 1);
       mbar_init(b_empty + 8 * s, 1);
     }
-    mbar_init(b_vt, 8);
-    mbar_init(b_vt + 8, 8);
+    mbar_init(b_vt, kOut ? 8 : 12);
+    mbar_init(b_vt + 8, 12);
     mbar_init(b_kv, 1);
     mbar_init(b_kv + 8, 1);
     mbar_init(b_s, 1);
-    mbar_init(b_s_read, 4);
+    mbar_init(b_kv_free, 8);
     mbar_init(b_h, 8);
     mbar_init(b_oi, 1);
     mbar_init(b_p, 4);
@@ -324,6 +366,23 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+
+  // (the set-up above touches no global memory and runs while the work before this one drains)
+  grid_dep_wait();
+  grid_dep_launch();
+  const int h = blockIdx.x, unit = blockIdx.y;
+  const Unit un = find_unit<kOut>(p, unit);
+  const int t_begin = un.t_begin, t_end = un.t_end;
+  const int n_chunks = (t_end - t_begin + C - 1) / C;
+  const float g = p.log_decay[h];
+  const float *state_in;
+  float *state_out;
+  p.st.resolve(un.seq, h, p.hv, &state_in, &state_out);
+  constexpr int64_t kState = static_cast<int64_t>(D) * D;
+  // a sequence's segments lie one behind the other in the workspace
+  float *ws = p.ws + (static_cast<int64_t>(un.first) * p.hv + h) * kState;
+  const int64_t ws_step = p.hv * kState;
+
   const auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
   // the same for all lanes of a warp: they go on, or give up, together
   const auto wait_warp = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
@@ -334,7 +393,22 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const auto kv_bar = [&](int c) { return kOut ? b_kv : b_kv + 8 * (c & 1); };
   const auto phase2 = [&](int c) { return kOut ? c : c >> 1; };
 
-  if (warp == 12) {
+  const auto landed = [&](int c) { return wait_warp(b_full + 8 * (c % kStages), c / kStages); };
+  const auto kv_done = [&](int c) {
+    if (!wait_warp(kv_bar(c), phase2(c))) return false;
+    tc_fence_after();
+    return true;
+  };
+  const auto vt_made = [&](int c) {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(vt_bar(c));
+  };
+
+  if (warp >= 12) {
+   regs_dec<kRegsFew>();
+   if (warp == 12) {
     if (lane == 0) {
       // ---- copies: chunk c into a stage once the products of the chunk before it there are done
       const int qk_col = (h / p.group) * D, v_col = h * D;
@@ -360,17 +434,21 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         mbar_wait(b_full + 8 * (c % kStages), (c / kStages) & 1, p.err, 1u << 16);
     }
     __syncwarp();
-  } else if (warp == 13) {
+   } else if (warp == 13) {
     // ---- products
     const bool elected = elect_one();
     // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
     const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
     const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
     const uint64_t dp = sdesc(sbase + OFF_P, 16, 1024);
-    for (int c = 0; c < n_chunks; ++c) {
+    const auto kv_ready = [&](int c) {   // KV(c) may be issued
+      return landed(c) && wait_warp(vt_bar(c), phase2(c)) &&
+             (!kOut || c == 0 || wait_warp(b_kv_free, c - 1));
+    };
+    bool go = n_chunks > 0 && kv_ready(0);
+    for (int c = 0; c < n_chunks && go; ++c) {
       const int s = c % kStages;
       const uint64_t st = static_cast<uint64_t>(s * STAGE) >> 4;
-      if (!wait_warp(b_full + 8 * s, c / kStages) || !wait_warp(vt_bar(c), phase2(c))) break;
       tc_fence_after();
       const uint32_t kv = kv_col(c), vt = vt_col(c);
       const uint64_t bk = dk_mn0 + st, aq = dq0 + st;
@@ -386,7 +464,12 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!kOut) mma_commit(b_empty + 8 * s);
       }
       __syncwarp();
-      if (!kOut) continue;
+      if (!kOut) {
+        go = c + 1 == n_chunks || kv_ready(c + 1);
+        continue;
+      }
+      if (c > 0 && !wait_warp(b_o_free, c - 1)) break;
+      tc_fence_after();
       if (elected) {
         // S(c) = Q K^T
         const uint64_t bks = dk0 + st;
@@ -398,7 +481,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         mma_commit(b_s);
       }
       __syncwarp();
-      if (!wait_warp(b_h, c) || (c > 0 && !wait_warp(b_o_free, c - 1))) break;
+      if (!wait_warp(b_h, c)) break;
       tc_fence_after();
       if (elected) {
         // OI(c) = H0^T Q^T
@@ -426,13 +509,16 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         mma_commit(b_empty + 8 * s);
       }
       __syncwarp();
+      go = c + 1 == n_chunks || kv_ready(c + 1);
     }
     if (elected) {
       mma_commit(b_drain);   // every product issued is complete before tensor memory is released
       mbar_wait(b_drain, 0, p.err, 1u << 20);
     }
     __syncwarp();
+   }
   } else if (warp < 4) {
+    regs_dec<kRegsOut>();
     if (kOut) {
       // ---- P(c) and o(c)
       // S as an M = 64 product: rows 16 w .. 16 w + 15 in lanes 32 w .. 32 w + 15; thread t takes row
@@ -468,9 +554,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           float sv[32];
           tmem_ld32x2(tmem + quarter + TC_S, sv);
           tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_s_read);
 #pragma unroll
           for (int v8 = 0; v8 < 4; ++v8) {
             uint32_t hi[4], lo[4];
@@ -487,6 +570,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             st_shared16(at + HALF, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         }
+        tc_fence_before();
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
@@ -547,16 +631,40 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
         }
       }
-      if (lane == 0) bulk_wait_all();
+      if (lane == 0) bulk_wait_read();   // the tiles are shared memory: not left before they are read
       __syncwarp();
+    } else {
+      // ---- without output: V' of tokens 0..31
+      const VPart<2> vp(g, lane, warp, 0);
+      for (int c = 0; c < n_chunks; ++c) {
+        if (!landed(c)) break;
+        float2 nf;
+        uint32_t w[2][24];
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) vp.template split<false>(sbase + (c % kStages) * STAGE + OFF_V, gr, lane, w[gr], nf);
+        if (c > 1 && !kv_done(c - 2)) break;   // its V' was in this buffer
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) vp.store(vt_col(c), gr, w[gr]);
+        vt_made(c);
+      }
     }
   } else {
     // ---- the state: thread = row dv of H^T, dk columns 64 half .. + 63; V' of tokens 32 half .. + 31
+    // (without output 32 + 16 half .. + 15)
+    regs_inc<kRegsState>();
     const int half = (warp - 4) >> 2, q4 = warp & 3;
     const int dv = 32 * q4 + lane;
     const uint32_t quarter = static_cast<uint32_t>(32 * q4) << 16;
+    constexpr int NB = kOut ? 2 : 1;
+    const int tok_base = kOut ? 32 * half : 32 + 16 * half;
+    VPart<NB> vp(g, lane, q4, tok_base);
     float2 H[32];
-    {
+    const DecayStep full_step = decay_step(g, C), last_step = decay_step(g, t_end - t_begin - (n_chunks - 1) * C);
+    // byte offset of (row 32 half + r, column dv) in a [64 tokens][128] tile
+    const auto elem = [&](int r) {
+      return (dv >> 6) * HALF + (32 * half + r) * 128 + ((((dv >> 3) & 7) ^ (r & 7)) << 4) + (dv & 7) * 2;
+    };
+    const auto load_h = [&]() {
       const int64_t at = static_cast<int64_t>(64 * half) * D + dv;
       if (un.seg == 0) {
         // (a split sequence's second launch reads the copy: another CTA may write state_out meanwhile)
@@ -587,130 +695,124 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
         }
       }
-    }
-    // V': this warp's 32 dv x 32 tokens as transposed 8 x 8 tiles.  Lane l gives the address of row
-    // l & 7 of tile l >> 3: token block (l >> 4), dv block (l >> 3) & 1; thread t holds tokens
-    // 32 half + 8 n + 2 (t % 4) and the next one of dv rows t / 4 + 8 b + 16 gr.
-    const uint32_t vrow = (q4 >> 1) * HALF + (32 * half + 8 * (lane >> 4) + (lane & 7)) * 128;
-    const uint32_t vchunk = 4 * (q4 & 1) + ((lane >> 3) & 1);
-    const int tok0 = 32 * half + 2 * (lane & 3);
-    float2 d[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-      d[n] = make_float2(decay_pow(g, C - 1 - (tok0 + 8 * n)), decay_pow(g, C - 2 - (tok0 + 8 * n)));
-    // byte offset of (row 32 half + r, column dv) in a [64 tokens][128] tile
-    const auto elem = [&](int r) {
-      return (dv >> 6) * HALF + (32 * half + r) * 128 + ((((dv >> 3) & 7) ^ (r & 7)) << 4) + (dv & 7) * 2;
     };
-    const DecayStep full_step = decay_step(g, C), last_step = decay_step(g, t_end - t_begin - (n_chunks - 1) * C);
-    const auto make_vt = [&](int c) {
-      const uint32_t st = sbase + (c % kStages) * STAGE;
-      const int len = min(C, t_end - t_begin - c * C);
-      if (len < C) {   // rows behind the end: zero in K and V, so that nothing there is multiplied
-#pragma unroll 1
-        for (int r = 0; r < 32; ++r)
-          if (32 * half + r >= len) {
-            st_shared_u16(st + OFF_V + elem(r), 0);
-            st_shared_u16(st + OFF_K + elem(r), 0);
-          }
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {   // (the last chunk: the others' factors are not needed any more)
-          const int left = len - 1 - (tok0 + 8 * n);
-          d[n] = make_float2(left >= 0 ? decay_pow(g, left) : 0.0f, left >= 1 ? decay_pow(g, left - 1) : 0.0f);
-        }
-      }
-      float2 nf = make_float2(0.0f, 0.0f);   // NaN once a value was not finite
-#pragma unroll
-      for (int gr = 0; gr < 2; ++gr) {
-        uint32_t raw[8], hi[8], mid[8], lo[8];
-        const uint32_t at = st + OFF_V + vrow + (((vchunk + 2 * gr) ^ (lane & 7)) << 4);
-        ldsm_x4_t(at, raw);
-        ldsm_x4_t(at + 16 * 128, raw + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {   // e = 2 n + b
-          const float2 v = make_float2(__uint_as_float(raw[e] << 16), __uint_as_float(raw[e] & 0xFFFF0000u));
-          if (kOut) nf = __ffma2_rn(v, make_float2(0.0f, 0.0f), nf);
-          const float2 x = __fmul2_rn(v, d[e >> 1]);
-          const float2 y = behind_tops(x);
-          const float2 z = behind_tops(y);
-          hi[e] = tops(x.x, x.y);
-          mid[e] = tops(y.x, y.y);
-          lo[e] = pack_pair(z.x, z.y);
-        }
-        const uint32_t vt = vt_col(c) + quarter + (static_cast<uint32_t>(16 * gr) << 16) + 16 * half;
-        tmem_st_16x128b_x4(vt, hi);
-        tmem_st_16x128b_x4(vt + VT_TERM, mid);
-        tmem_st_16x128b_x4(vt + 2 * VT_TERM, lo);
-      }
-      bool wrote = len < C;
-      if (kOut && __any_sync(0xffffffffu, nf.x != nf.x || nf.y != nf.y)) {
-        // PV multiplies every value of the chunk, by zero where it is still to come: take what is not
-        // finite out of the tile and tell warps 0..3 from which token on this dv is not finite
-        int first = 0xFF;
-#pragma unroll 1
-        for (int r = 31; r >= 0; --r) {
-          const uint32_t at = st + OFF_V + elem(r);
-          if ((ld_shared_u16(at) & 0x7F80u) == 0x7F80u) {
-            st_shared_u16(at, 0);
-            first = 32 * half + r;
-          }
-        }
-        bad[(c & 3) * 2 * D + half * D + dv] = static_cast<uint8_t>(first);
-        wrote = true;
-      }
-      if (wrote) fence_proxy_async();
-      __syncwarp();
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(vt_bar(c));
-    };
-    const auto take_kv = [&](int c) {   // H <- l^n H + KV(c)
-      if (!wait_warp(kv_bar(c), phase2(c))) return false;
-      tc_fence_after();
+    const auto take_kv = [&](int c) {   // H <- l^n H + KV(c), KV(c) being done
       const DecayStep now = c < n_chunks - 1 ? full_step : last_step;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         float kv[32];
         tmem_ld32(kv_col(c) + quarter + 64 * half + 32 * part, kv);
         tmem_wait_ld();
+        if (kOut && part == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_kv_free);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           H[16 * part + e] = now.apply2(H[16 * part + e], make_float2(kv[2 * e], kv[2 * e + 1]));
       }
-      return true;
     };
     bool go = true;
-    for (int c = 0; c < n_chunks; ++c) {
-      go = wait_warp(b_full + 8 * (c % kStages), c / kStages) && (!kOut || c == 0 || wait_warp(b_s_read, c - 1));
-      if (!go) break;
-      tc_fence_after();
-      make_vt(c);
-      if (kOut) {
-        // H before chunk c, once OI(c - 1) has read the one before
-        if (c > 0 && !(go = wait_warp(b_oi, c - 1))) break;
-        tc_fence_after();
-        uint32_t w[32];
+    float2 nf = make_float2(0.0f, 0.0f);
+    if constexpr (kOut) {
+      uint32_t w[24];
+      // V'(c) in two parts: what is done before its columns are free, and the rest
+      const auto begin_vt = [&](int c) {
+        const uint32_t st = sbase + (c % kStages) * STAGE;
+        const int len = min(C, t_end - t_begin - c * C);
+        if (len < C) {   // rows behind the end: zero in K and V, so that nothing there is multiplied
+#pragma unroll 1
+          for (int r = 0; r < 32; ++r)
+            if (32 * half + r >= len) {
+              st_shared_u16(st + OFF_V + elem(r), 0);
+              st_shared_u16(st + OFF_K + elem(r), 0);
+            }
+          fence_proxy_async();
+          __syncwarp();
+          vp.factors(g, len);   // (the last chunk: the others' are not needed any more)
+        }
+        nf = make_float2(0.0f, 0.0f);
+        vp.template split<true>(st + OFF_V, 0, lane, w, nf);
+      };
+      const auto finish_vt = [&](int c) {
+        const uint32_t st = sbase + (c % kStages) * STAGE;
+        vp.store(vt_col(c), 0, w);
+        vp.template split<true>(st + OFF_V, 1, lane, w, nf);
+        vp.store(vt_col(c), 1, w);
+        if (__any_sync(0xffffffffu, nf.x != nf.x || nf.y != nf.y)) {
+          // PV multiplies every value of the chunk, by zero where it is still to come: take what is not
+          // finite out of the tile and tell warps 0..3 from which token on this dv is not finite
+          int first = 0xFF;
+#pragma unroll 1
+          for (int r = 31; r >= 0; --r) {
+            const uint32_t at = st + OFF_V + elem(r);
+            if ((ld_shared_u16(at) & 0x7F80u) == 0x7F80u) {
+              st_shared_u16(at, 0);
+              first = 32 * half + r;
+            }
+          }
+          bad[(c & 3) * 2 * D + half * D + dv] = static_cast<uint8_t>(first);
+          fence_proxy_async();
+          __syncwarp();
+        }
+        vt_made(c);
+      };
+      const auto put_h = [&]() {   // H before a chunk -> TMEM
+        uint32_t x[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = tops(H[e].x, H[e].y);
-        tmem_st32(tmem + quarter + TC_H + 32 * half, w);
+        for (int e = 0; e < 32; ++e) x[e] = tops(H[e].x, H[e].y);
+        tmem_st32(tmem + quarter + TC_H + 32 * half, x);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float2 y = behind_tops(H[e]);
-          w[e] = pack_pair(y.x, y.y);
+          x[e] = pack_pair(y.x, y.y);
         }
-        tmem_st32(tmem + quarter + TC_H + 64 + 32 * half, w);
+        tmem_st32(tmem + quarter + TC_H + 64 + 32 * half, x);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_h);
-        if (!(go = take_kv(c))) break;
-      } else if (c > 0) {
-        if (!(go = take_kv(c - 1))) break;
+      };
+      if (n_chunks > 0 && (go = landed(0))) {
+        begin_vt(0);
+        finish_vt(0);
       }
+      if (go) load_h();   // (KV(0) and S(0) need no state)
+      if (n_chunks > 0 && go) put_h();
+      for (int c = 0; c < n_chunks && go; ++c) {
+        // while the products of chunk c run: V'(c + 1) first, which KV(c + 1) waits for
+        const bool more = c + 1 < n_chunks;
+        if (more) {
+          if (!(go = landed(c + 1))) break;
+          begin_vt(c + 1);
+        }
+        if (!(go = kv_done(c))) break;
+        if (more) finish_vt(c + 1);
+        take_kv(c);
+        if (more) {
+          if (!(go = wait_warp(b_oi, c))) break;
+          tc_fence_after();
+          put_h();
+        }
+      }
+    } else {
+      load_h();
+      for (int c = 0; c < n_chunks; ++c) {   // V'(c) while KV(c - 1) runs
+        if (!(go = landed(c))) break;
+        uint32_t w[2][12];
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) vp.template split<false>(sbase + (c % kStages) * STAGE + OFF_V, gr, lane, w[gr], nf);
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) vp.store(vt_col(c), gr, w[gr]);
+        vt_made(c);
+        if (c > 0) {
+          if (!(go = kv_done(c - 1))) break;
+          take_kv(c - 1);
+        }
+      }
+      if (n_chunks > 0 && go && (go = kv_done(n_chunks - 1))) take_kv(n_chunks - 1);
     }
-    if (!kOut && go) go = take_kv(n_chunks - 1);
     float *dst = !kOut ? ws + un.seg * ws_step : un.seg == un.segs - 1 ? state_out : nullptr;
     if (go && dst) {
       dst += static_cast<int64_t>(64 * half) * D + dv;
@@ -729,47 +831,71 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 // Chunks of a segment (0: no sequence is split) and the number of units.
 struct DecayPlan {
   int seg_chunks;
-  int units;
+  int units;   // segments
+  int early;   // segments that are not their sequence's last
 };
 
-// With units = (sequence, segment) x heads on 148 SMs, one at a time on each, a launch takes the
-// longest unit, or, when there are more units than SMs, about the mean load plus half a unit.
-// Times in chunks; the state-only launch takes 0.45 of a chunk for each of its chunks, and a split
-// costs another launch, the states' way through memory and 0.6 of a chunk for each earlier segment.
-DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
-  DecayPlan best{0, n_seqs};
-  if (static_cast<int64_t>(n_seqs) * hv > 4 * kSms) return best;   // enough units as it is
-  int longest = 0;
-  int64_t chunks = 0;
-  for (int n = 0; n < n_seqs; ++n) {
-    const int nc = static_cast<int>((static_cast<int64_t>(cu[n + 1]) - cu[n] + C - 1) / C);
-    longest = std::max(longest, nc);
-    chunks += nc;
-  }
-  const auto launch_time = [&](int64_t units, int64_t load, int unit) {
-    return units <= kSms ? static_cast<double>(unit)
-                         : std::max<double>(unit, static_cast<double>(load) / kSms + 0.5 * unit);
-  };
-  double least = launch_time(static_cast<int64_t>(n_seqs) * hv, chunks * hv, longest);
-  for (int s = 2; s <= 32; ++s) {
-    const int len = (longest + s - 1) / s;
-    if (len < 4) break;
-    int units = 0, split = 0, most = 1;
-    int64_t early = 0;
-    for (int n = 0; n < n_seqs; ++n) {
-      const int nc = static_cast<int>((static_cast<int64_t>(cu[n + 1]) - cu[n] + C - 1) / C);
-      const int segs = std::max(1, (nc + len - 1) / len);
-      units += segs;
-      split += segs - 1;
-      early += static_cast<int64_t>(segs - 1) * len;
-      most = std::max(most, segs);
+// How long a launch takes whose units (count heads x a length in chunks each, the longest first) go
+// to 148 SMs, one at a time on each, the next one to the SM that is free first.
+struct Launch {
+  double at[kMostSplit * 32 + 1];   // SMs by the time they are free, ascending
+  int sms[kMostSplit * 32 + 1];
+  int n;
+  Launch() : n(1) { at[0] = 0.0, sms[0] = kSms; }
+  void add(int units, double chunks) {
+    while (units > 0) {
+      const int m = std::min(units, sms[0]);
+      const double t = at[0] + chunks;
+      if ((sms[0] -= m) == 0) {
+        --n;
+        std::copy(at + 1, at + 1 + n, at);
+        std::copy(sms + 1, sms + 1 + n, sms);
+      }
+      int i = n;
+      while (i > 0 && at[i - 1] > t) --i;
+      if (i > 0 && at[i - 1] == t) {
+        sms[i - 1] += m;
+      } else {
+        std::copy_backward(at + i, at + n, at + n + 1);
+        std::copy_backward(sms + i, sms + n, sms + n + 1);
+        at[i] = t, sms[i] = m, ++n;
+      }
+      units -= m;
     }
-    const double t = launch_time(static_cast<int64_t>(units) * hv, chunks * hv, len) +
-                     0.45 * launch_time(static_cast<int64_t>(split) * hv, early * hv, len) + 4.0 + 0.6 * (most - 1);
+  }
+  double time() const { return at[n - 1]; }
+};
+
+int chunks_of(const int32_t *cu, int n) {
+  return static_cast<int>((static_cast<int64_t>(cu[n + 1]) - cu[n] + C - 1) / C);
+}
+
+// Splitting pays when few (sequence, head) units leave SMs idle.  Times in chunks of the main launch
+// (3200 cycles): the state-only launch takes 0.42 of one for each of its chunks, and a split costs
+// another launch (4) and the earlier segments' states for each segment (0.6 for each).
+DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
+  DecayPlan best{0, n_seqs, 0};
+  if (n_seqs > kMostSplit || static_cast<int64_t>(n_seqs) * hv > 2 * kSms) return best;
+  int nc[kMostSplit];
+  for (int n = 0; n < n_seqs; ++n) nc[n] = chunks_of(cu, n);
+  std::sort(nc, nc + n_seqs, [](int a, int b) { return a > b; });
+  Launch whole;
+  for (int n = 0; n < n_seqs; ++n) whole.add(hv, nc[n]);
+  double least = whole.time();
+  for (int s = 2; s <= 32; ++s) {
+    const int len = (nc[0] + s - 1) / s;
+    if (len < 4) break;
+    Launch main, early;
+    int units = 0, split = 0;
+    for (int n = 0; n < n_seqs; ++n) units += std::max(1, (nc[n] + len - 1) / len);
+    split = units - n_seqs;
+    main.add(split * hv, len);
+    early.add(split * hv, 0.42 * len);
+    for (int n = 0; n < n_seqs; ++n) main.add(hv, nc[n] > 0 ? (nc[n] - 1) % len + 1 : 0);
+    const double t = main.time() + early.time() + 4.0 + 0.6 * (s - 1);
     if (t < least) {
       least = t;
-      best.seg_chunks = len;
-      best.units = units;
+      best = DecayPlan{len, units, split};
     }
   }
   return best;
@@ -832,17 +958,31 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   p.group = hv / hk;
   p.n_seqs = n_seqs;
   p.seg_chunks = plan.seg_chunks;
+  if (n_seqs <= kListed) {
+    // (eight prompts of 1 to 7777 tokens, the longest the sixth: 437 us in their own order, 317 us so)
+    for (int n = 0; n < n_seqs; ++n) p.seq[n] = static_cast<uint8_t>(n);
+    std::stable_sort(p.seq, p.seq + n_seqs, [&](uint8_t a, uint8_t b) {
+      return cu_host[a + 1] - cu_host[a] > cu_host[b + 1] - cu_host[b];
+    });
+    int segs = 0;
+    for (int n = 0; n < n_seqs; ++n) {
+      p.begin[n] = cu_host[p.seq[n]];
+      p.end[n] = cu_host[p.seq[n] + 1];
+      if (plan.seg_chunks == 0) continue;
+      p.first[n] = static_cast<int16_t>(segs);
+      segs += std::max(1, (chunks_of(cu_host, p.seq[n]) + plan.seg_chunks - 1) / plan.seg_chunks);
+    }
+  }
   p.st = states;
   p.ws = static_cast<float *>(workspace);
   p.o = static_cast<uint16_t *>(o);
   p.err = device_error_ptr();
-  const dim3 grid(hv, plan.units);
   if (plan.seg_chunks != 0) {
-    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
+    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, dim3(hv, plan.early), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
                                  "decay prefill: segment kernel launch");
     if (st) return st;
   }
-  return launch_status(launch_pdl(decay_prefill_kernel<true>, grid, dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
+  return launch_status(launch_pdl(decay_prefill_kernel<true>, dim3(hv, plan.units), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
                        "decay prefill: kernel launch");
 }
 
