@@ -455,47 +455,106 @@ def linear(x, w, y=None, stream=None):
     return y
 
 
-def _heads(t, name, rows, heads=None):
-    """(pointer, token stride) of a bf16 [rows, heads, 128] CUDA tensor whose last two dims are dense."""
-    torch = _torch()
-    ptr = _ptr(t, torch.bfloat16, name, rows=True)
-    if t.shape[2] != HEAD_DIM or t.shape[0] < rows or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {HEAD_DIM}], got {tuple(t.shape)}")
-    # the stride of a dimension of one row means nothing: take it as dense
-    return ptr, (int(t.stride(0)) if t.shape[0] > 1 else 0)
+# The calls below are short enough on the device for the marshalling to show: one pass over the
+# tensors, the device entered only when it is not the current one.
+
+class _Call:
+    """Device and stream of a call, taken from its first tensor; every other must be there too."""
+    __slots__ = ("torch", "index")
+
+    def __init__(self, t, name):
+        self.torch = torch = _torch()
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        self.index = t.get_device()
+
+    def check(self, t, dtype, name):
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.index:   # -1 for the host
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"tensors on cuda:{self.index} and {t.device}: all tensors of a call must be on one device")
+
+    def dense(self, t, dtype, name, shape):
+        """Pointer of a contiguous tensor of that shape (None passes)."""
+        if t is None:
+            return None
+        self.check(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def heads(self, t, name, rows, heads):
+        """(pointer, token stride) of a bf16 [>= rows, heads, 128] tensor whose last two dims are dense."""
+        self.check(t, self.torch.bfloat16, name)
+        if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.shape[1] != heads or t.shape[0] < rows:
+            raise ValueError(f"{name} must be [{rows}, {heads}, {HEAD_DIM}], got {tuple(t.shape)}")
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        st = t.stride()
+        if st[2] != 1 or (heads > 1 and st[1] != HEAD_DIM) or st[0] < heads * HEAD_DIM:
+            raise ValueError(f"{name} must be [T, heads, 128] with dense rows that do not overlap")
+        return t.data_ptr(), st[0]
+
+    def rows(self, t, dtype, name, rows, d):
+        """(pointer, row stride) of `rows` rows of d values: contiguous, or [rows, d] with dense rows."""
+        if t is None:
+            return None, 0
+        self.check(t, dtype, name)
+        if t.numel() != rows * d or t.shape[-1] != d:
+            raise ValueError(f"{name} must hold {rows} rows of {d} values, got {tuple(t.shape)}")
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < d:
+            raise ValueError(f"{name} must be contiguous, or [rows, d] with dense rows that do not overlap")
+        return t.data_ptr(), t.stride(0)
+
+    def run(self, name, fn, stream, *args):
+        """fn(*args, stream) on the call's device."""
+        torch = self.torch
+        if stream is None:
+            handle = torch.cuda.current_stream(self.index).cuda_stream
+        else:
+            if getattr(stream, "device", None) is not None and stream.device.index != self.index:
+                raise ValueError(f"stream on {stream.device}, tensors on cuda:{self.index}")
+            handle = stream.cuda_stream
+        if torch.cuda.current_device() == self.index:
+            code = fn(*args, handle)
+        else:
+            with torch.cuda.device(self.index):
+                code = fn(*args, handle)
+        if code != 0:
+            raise GdrError(name, code)
 
 
 def _decay_inputs(q, k, v, log_decay, rows):
-    """Checked arguments shared by the decayed linear attention calls, in the ABI's order."""
-    torch = _torch()
-    (qp, qs), (vp, vs) = _heads(q, "q", rows), _heads(v, "v", rows)
+    """The call and the checked arguments the decayed linear attention calls share, in the ABI's order."""
+    call = _Call(q, "q")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must be [T, heads, 128]")
     hk, hv = int(q.shape[1]), int(v.shape[1])
-    kp, ks = _heads(k, "k", rows, hk)
-    if tuple(log_decay.shape) != (hv,):
-        raise ValueError(f"log_decay must have shape ({hv},), got {tuple(log_decay.shape)}")
-    return (qp, kp, vp, qs, ks, vs, _ptr(log_decay, torch.float32, "log_decay")), hk, hv
+    qp, qs = call.heads(q, "q", rows, hk)
+    kp, ks = call.heads(k, "k", rows, hk)
+    vp, vs = call.heads(v, "v", rows, hv)
+    return call, (qp, kp, vp, qs, ks, vs, call.dense(log_decay, _torch().float32, "log_decay", (hv,))), hk, hv
 
 
-def _states(t, name, entries, hv):
-    """Pointer of an fp32 [entries, hv, 128, 128] CUDA tensor (None passes)."""
-    if t is not None and tuple(t.shape) != (entries, hv, HEAD_DIM, HEAD_DIM):
-        raise ValueError(f"{name} must be [{entries}, {hv}, {HEAD_DIM}, {HEAD_DIM}], got {tuple(t.shape)}")
-    return _ptr(t, _torch().float32, name)
-
-
-def _decay_o(o, v, hv, rows):
+def _decay_o(call, o, v, hv, rows):
+    """o (made when None) and its pointer; it may have more rows than the call writes."""
     torch = _torch()
     if o is None:
         o = torch.empty((v.shape[0], hv, HEAD_DIM), dtype=torch.bfloat16, device=v.device)
-    elif o.dim() != 3 or o.shape[0] < rows or tuple(o.shape[1:]) != (hv, HEAD_DIM):
+        return o, o.data_ptr()
+    if isinstance(o, torch.Tensor) and (o.dim() != 3 or o.shape[0] < rows):
         raise ValueError(f"o must be [{rows}, {hv}, {HEAD_DIM}], got {tuple(o.shape)}")
-    return o
-
-
-def _slot_ptr(slot, rows):
-    if tuple(slot.shape) != (rows,):
-        raise ValueError(f"slot must have shape ({rows},), got {tuple(slot.shape)}")
-    return _ptr(slot, _torch().int32, "slot")
+    return o, call.dense(o, torch.bfloat16, "o", (o.shape[0], hv, HEAD_DIM))
 
 
 def decay_attn_workspace(cu_seqlens_host, hv: int, device):
@@ -506,19 +565,22 @@ def decay_attn_workspace(cu_seqlens_host, hv: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
-def _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, o, workspace):
+def _decay_prefill(name, q, k, v, log_decay, cu_seqlens, cu_seqlens_host, states, o, scale, workspace, stream):
+    """The prefill call `name`; states(call, n, hv) gives its arguments between n_seqs and o."""
     torch = _torch()
     cu, cup = _host_cu(cu_seqlens_host)
     if cu.ndim != 1 or cu.shape[0] < 1:
         raise ValueError("cu_seqlens_host must hold n_seqs + 1 offsets")
-    if tuple(cu_seqlens.shape) != cu.shape:
-        raise ValueError(f"cu_seqlens must have shape {cu.shape}, got {tuple(cu_seqlens.shape)}")
-    ins, hk, hv = _decay_inputs(q, k, v, log_decay, int(cu[-1]))
-    o = _decay_o(o, v, hv, int(cu[-1]))
+    n, total = cu.shape[0] - 1, int(cu[-1])
+    call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, total)
+    o, op = _decay_o(call, o, v, hv, total)
     if workspace is None:
         workspace = decay_attn_workspace(cu, hv, v.device)
-    ws = (_ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else int(workspace.numel()))
-    return ins, hk, hv, cu, cup, o, workspace, ws
+    wp, wbytes = (None, 0) if workspace is None else (
+        call.dense(workspace, torch.uint8, "workspace", workspace.shape), workspace.numel())
+    call.run(name, getattr(lib(), name), stream, *ins, float(scale), hk, hv,
+             call.dense(cu_seqlens, torch.int32, "cu_seqlens", cu.shape), cup, n, *states(call, n, hv), op, wp, wbytes)
+    return o
 
 
 def decay_attn_prefill(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, h0=None, hT=None, o=None,
@@ -526,18 +588,16 @@ def decay_attn_prefill(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, h0=None,
     """Decayed linear attention over packed sequences: H_t = exp(log_decay) H_{t-1} + k_t v_t^T,
     o_t = scale H_t^T q_t.  q, k [T, hk, 128], v [T, hv, 128] bf16 (token-strided views allowed),
     log_decay [hv] fp32.  Returns o [T, hv, 128] bf16 (and writes hT [N, hv, 128, 128] fp32 when
-    given); rows of o behind the last sequence are left as they were."""
-    torch = _torch()
-    ins, hk, hv, cu, cup, o, workspace, ws = _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host,
-                                                                  o, workspace)
-    n = cu.shape[0] - 1
-    dev = _device_of(q, k, v, log_decay, cu_seqlens, h0, hT, o, workspace)
-    with torch.cuda.device(dev):
-        _check("gdr_decay_attn_prefill", lib().gdr_decay_attn_prefill(
-            *ins, float(scale), hk, hv, _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cup, n,
-            _states(h0, "h0", n, hv), _states(hT, "hT", n, hv), _ptr(o, torch.bfloat16, "o"), *ws,
-            _stream(stream, dev)))
-    return o
+    given); rows of o behind the last sequence are left as they were.  Without a workspace one is
+    made for the call when it needs one (decay_attn_workspace); a captured graph, or calls on
+    several streams, should each be given their own."""
+    f32 = _torch().float32
+
+    def states(call, n, hv):
+        shape = (n, hv, HEAD_DIM, HEAD_DIM)
+        return call.dense(h0, f32, "h0", shape), call.dense(hT, f32, "hT", shape)
+    return _decay_prefill("gdr_decay_attn_prefill", q, k, v, log_decay, cu_seqlens, cu_seqlens_host, states, o, scale,
+                          workspace, stream)
 
 
 def decay_attn_prefill_slots(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, state_pool, slot,
@@ -547,30 +607,23 @@ def decay_attn_prefill_slots(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, st
     state_pool (or from zero, init_from_pool=False) and leaves its final state there.  A slot
     outside the pool is a sequence that starts from zero and keeps no state."""
     torch = _torch()
-    ins, hk, hv, cu, cup, o, workspace, ws = _decay_prefill_setup(q, k, v, log_decay, cu_seqlens, cu_seqlens_host,
-                                                                  o, workspace)
-    n, n_slots = cu.shape[0] - 1, int(state_pool.shape[0])
-    dev = _device_of(q, k, v, log_decay, cu_seqlens, state_pool, slot, o, workspace)
-    with torch.cuda.device(dev):
-        _check("gdr_decay_attn_prefill_slots", lib().gdr_decay_attn_prefill_slots(
-            *ins, float(scale), hk, hv, _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cup, n,
-            _states(state_pool, "state_pool", n_slots, hv), n_slots, _slot_ptr(slot, n),
-            int(bool(init_from_pool)), _ptr(o, torch.bfloat16, "o"), *ws, _stream(stream, dev)))
-    return o
+    n_slots = int(state_pool.shape[0])
+
+    def states(call, n, hv):
+        return (call.dense(state_pool, torch.float32, "state_pool", (n_slots, hv, HEAD_DIM, HEAD_DIM)), n_slots,
+                call.dense(slot, torch.int32, "slot", (n,)), int(bool(init_from_pool)))
+    return _decay_prefill("gdr_decay_attn_prefill_slots", q, k, v, log_decay, cu_seqlens, cu_seqlens_host, states, o,
+                          scale, workspace, stream)
 
 
 def decay_attn_decode(q, k, v, log_decay, state, o=None, scale: float = 1.0, stream=None):
     """One token of decayed linear attention for each of B sequences; q, k [B, hk, 128],
     v [B, hv, 128] bf16, state [B, hv, 128, 128] fp32 updated in place -> o [B, hv, 128] bf16."""
-    torch = _torch()
     B = int(v.shape[0])
-    ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
-    o = _decay_o(o, v, hv, B)
-    dev = _device_of(q, k, v, log_decay, state, o)
-    with torch.cuda.device(dev):
-        _check("gdr_decay_attn_decode", lib().gdr_decay_attn_decode(
-            *ins, float(scale), hk, hv, _states(state, "state", B, hv), _ptr(o, torch.bfloat16, "o"), B,
-            _stream(stream, dev)))
+    call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
+    o, op = _decay_o(call, o, v, hv, B)
+    call.run("gdr_decay_attn_decode", lib().gdr_decay_attn_decode, stream, *ins, float(scale), hk, hv,
+             call.dense(state, _torch().float32, "state", (B, hv, HEAD_DIM, HEAD_DIM)), op, B)
     return o
 
 
@@ -579,33 +632,12 @@ def decay_attn_decode_slots(q, k, v, log_decay, state_pool, slot, o=None, scale:
     outside the pool is a padding row (zero o)."""
     torch = _torch()
     B, n_slots = int(v.shape[0]), int(state_pool.shape[0])
-    ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
-    o = _decay_o(o, v, hv, B)
-    dev = _device_of(q, k, v, log_decay, state_pool, slot, o)
-    with torch.cuda.device(dev):
-        _check("gdr_decay_attn_decode_slots", lib().gdr_decay_attn_decode_slots(
-            *ins, float(scale), hk, hv, _states(state_pool, "state_pool", n_slots, hv), n_slots,
-            _slot_ptr(slot, B), _ptr(o, torch.bfloat16, "o"), B, _stream(stream, dev)))
+    call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
+    o, op = _decay_o(call, o, v, hv, B)
+    call.run("gdr_decay_attn_decode_slots", lib().gdr_decay_attn_decode_slots, stream, *ins, float(scale), hk, hv,
+             call.dense(state_pool, torch.float32, "state_pool", (n_slots, hv, HEAD_DIM, HEAD_DIM)), n_slots,
+             call.dense(slot, torch.int32, "slot", (B,)), op, B)
     return o
-
-
-def _row_view(t, name, dtype, rows, d):
-    """(pointer, row stride) of a CUDA tensor of `rows` rows of d values: contiguous, or [rows, d]
-    with dense rows.  (None, 0) for None."""
-    if t is None:
-        return None, 0
-    torch = _torch()
-    if isinstance(t, torch.Tensor) and t.numel() != rows * d or t.shape[-1] != d:
-        raise ValueError(f"{name} must hold {rows} rows of {d} values, got {tuple(t.shape)}")
-    if t.dim() == 2 and t.stride(1) == 1 and rows > 1 and not t.is_contiguous():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.stride(0) < d:
-            raise ValueError(f"{name} must have rows that do not overlap")
-        return t.data_ptr(), int(t.stride(0))
-    return _ptr(t, dtype, name), 0
 
 
 def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None, w_pre=None, alpha: float = 1.0,
@@ -619,35 +651,26 @@ def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None
     (None) when no tensor is given for it."""
     torch = _torch()
     bf, f32 = torch.bfloat16, torch.float32
-    d = int(x.shape[-1])
+    call = _Call(x, "x")
+    d = int(x.shape[-1]) if x.dim() else 0
     rows = x.numel() // d if d else 0
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else bf
-    if rdt not in (bf, f32):
+    if rdt != bf and rdt != f32:
         raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {rdt}")
     if residual_out is None and want_residual:
         residual_out = torch.empty(x.shape, dtype=rdt, device=x.device)
     if y is None and want_y:
         y = torch.empty(x.shape, dtype=bf, device=x.device)
-    a = BlockNormArgs()
-    a.x, a.x_stride = _row_view(x, "x", bf, rows, d)
-    a.post_norm, a.eps_post = int(bool(post_norm)), float(eps if eps_post is None else eps_post)
-    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-        if w is not None and tuple(w.shape) != (d,):
-            raise ValueError(f"{name} must have shape ({d},), got {tuple(w.shape)}")
-        setattr(a, name, _ptr(w, f32, name))
-    if gate is not None and gate.dim() == 1:
-        a.gate, _ = _row_view(gate, "gate", bf, 1, d)
-        a.gate_shared = 1
-    else:
-        a.gate, a.gate_stride = _row_view(gate, "gate", bf, rows, d)
-    a.alpha, a.eps_pre = float(alpha), float(eps)
-    a.residual, a.residual_stride = _row_view(residual, "residual", rdt, rows, d)
-    a.residual_out, a.residual_out_stride = _row_view(residual_out, "residual_out", rdt, rows, d)
-    a.residual_fp32 = int(rdt == f32)
-    a.y, a.y_stride = _row_view(y, "y", bf, rows, d)
-    dev = _device_of(x, residual, gate, w_post, w_pre, residual_out, y)
-    with torch.cuda.device(dev):
-        _check("gdr_block_norm", lib().gdr_block_norm(ctypes.byref(a), rows, d, _stream(stream, dev)))
+    shared = gate is not None and gate.dim() == 1
+    xp, xs = call.rows(x, bf, "x", rows, d)
+    gp, gs = call.rows(gate, bf, "gate", 1 if shared else rows, d)
+    rp, rs = call.rows(residual, rdt, "residual", rows, d)
+    op, os_ = call.rows(residual_out, rdt, "residual_out", rows, d)
+    yp, ys = call.rows(y, bf, "y", rows, d)
+    args = BlockNormArgs(xp, xs, 1 if post_norm else 0, call.dense(w_post, f32, "w_post", (d,)),
+                         eps if eps_post is None else eps_post, gp, gs, 1 if shared else 0, alpha, rp, rs,
+                         1 if rdt == f32 else 0, op, os_, call.dense(w_pre, f32, "w_pre", (d,)), eps, yp, ys)
+    call.run("gdr_block_norm", lib().gdr_block_norm, stream, ctypes.byref(args), rows, d)
     return residual_out, y
 
 

@@ -7,8 +7,10 @@
 // in fp32; y is made from the unrounded r.  Memory-bound: x, the residual and a gate of
 // every row are read once, the new residual and y written once.
 //
-// One CTA per row; thread t holds the 8-value vectors t, t + blockDim, ... of the row in
-// registers, so the row is read once although both norms need all of it.
+// A row is held in registers, so it is read once although both norms need all of it, and all
+// its loads are issued before the first sum.  Up to 1024 values a warp holds a row (32 values
+// a lane at most) and sums with shuffles alone; above, a CTA of up to 512 threads does, 16 values
+// a thread up to 8192, 32 up to 16384, 64 above.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,110 +20,166 @@
 namespace gdr {
 namespace {
 
-constexpr int kVec = 4;   // 8-value vectors a thread can hold
+constexpr int kWarpRows = 4;   // rows (warps) of a CTA where a warp holds a row
 
-__device__ __forceinline__ float block_sum(float v, float *s_part) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  __syncthreads();   // the last sum's reads are done
-  if ((threadIdx.x & 31) == 0) s_part[warp] = v;
-  __syncthreads();
-  float t = 0.0f;
-  for (int w = 0; w < warps; ++w) t += s_part[w];
-  return t;
+  return v;
 }
 
-__device__ __forceinline__ void load_f8(const float *p, float *f) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+// Sum over the warp (kWarp) or the CTA; `part` is 32 floats of shared memory of this sum alone.
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float *part) {
+  v = warp_sum(v);
+  if (kWarp) return v;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? part[lane] : 0.0f);
+}
+
+__device__ __forceinline__ void mul8(float *r, const float *m) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] *= m[e];
+}
+__device__ __forceinline__ void get8(const float4 *p, float *f) {
+  const float4 a = __ldg(p), b = __ldg(p + 1);
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
+__device__ __forceinline__ float sum_sq8(const float *f) {
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += f[e] * f[e];
+  return s;
+}
 
-__global__ void block_norm_kernel(const BlockNormParams p) {
-  __shared__ float s_part[32];
+// Thread t of a row's `width` threads holds the 8-value vectors t, t + width, ... (NV of them).
+template <int NV, bool kWarp, bool kPost, bool kWide>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 512)
+block_norm_kernel(const __grid_constant__ BlockNormParams p) {
+  __shared__ float s_part[2][32];
+  const int width = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  const int nv = p.d >> 3;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t row = blockIdx.x;
-  const int nv = p.d >> 3;
-  float r[kVec][8];
-  const uint16_t *x = p.x + row * p.x_stride;
+  if (kWarp && row >= p.rows) return;
+
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 x[NV], gate[NV], res[NV * (kWide ? 2 : 1)];
+  const uint4 *px = reinterpret_cast<const uint4 *>(p.x + row * p.x_stride);
+  const uint4 *pg = reinterpret_cast<const uint4 *>(p.gate + row * p.gate_stride);
+  const uint4 *pr = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.res) + row * p.res_stride * (kWide ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * width;
+    const bool in = c < nv;
+    x[i] = in ? px[c] : zero;
+    if (p.res) {
+      if (kWide) {
+        res[2 * i] = in ? pr[2 * c] : zero;
+        res[2 * i + 1] = in ? pr[2 * c + 1] : zero;
+      } else {
+        res[i] = in ? pr[c] : zero;
+      }
+    }
+    if (p.gate) gate[i] = in ? pg[c] : zero;
+  }
+
+  float r[NV][8];
+  float f = p.alpha;
+  if (kPost) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      unpack8(x[i], r[i]);
+      ss += sum_sq8(r[i]);
+    }
+    f *= 1.0f / sqrtf(row_sum<kWarp>(ss, s_part[0]) / static_cast<float>(p.d) + p.eps_post);
+  }
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nv) {
-      unpack8(*reinterpret_cast<const uint4 *>(x + 8 * c), r[i]);
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * width;
+    if (c >= nv) continue;
+    float m[8];
+    if (!kPost) unpack8(x[i], r[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += r[i][e] * r[i][e];
+    for (int e = 0; e < 8; ++e) r[i][e] *= f;
+    if (kPost && p.w_post) {
+      get8(reinterpret_cast<const float4 *>(p.w_post) + 2 * c, m);
+      mul8(r[i], m);
     }
-  }
-  float f = p.alpha;
-  if (p.post) f *= 1.0f / sqrtf(block_sum(ss, s_part) / static_cast<float>(p.d) + p.eps_post);
-  ss = 0.0f;
+    if (p.gate) {
+      unpack8(gate[i], m);
+      mul8(r[i], m);
+    }
+    if (p.res) {
+      if (kWide) {
+        const uint4 a = res[2 * i], b = res[2 * i + 1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nv) {
-      float m[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[i][e] *= f;
-      if (p.post && p.w_post) {
-        load_f8(p.w_post + 8 * c, m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] *= m[e];
-      }
-      if (p.gate) {
-        unpack8(*reinterpret_cast<const uint4 *>(p.gate + row * p.gate_stride + 8 * c), m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] *= m[e];
-      }
-      if (p.res) {
-        if (p.res_fp32) load_f8(static_cast<const float *>(p.res) + row * p.res_stride + 8 * c, m);
-        else unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.res) + row * p.res_stride + 8 * c), m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] += m[e];
-      }
-      if (p.out) {
-        if (p.res_fp32) {
-          float *w = static_cast<float *>(p.out) + row * p.out_stride + 8 * c;
-          *reinterpret_cast<float4 *>(w) = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-          *reinterpret_cast<float4 *>(w + 4) = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
-        } else {
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * p.out_stride + 8 * c) = pack8x2(r[i]);
-        }
+        for (int e = 0; e < 8; ++e) m[e] = __uint_as_float(w[e]);
+      } else {
+        unpack8(res[i], m);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += r[i][e] * r[i][e];
+      for (int e = 0; e < 8; ++e) r[i][e] += m[e];
+    }
+    ss += sum_sq8(r[i]);
+    if (p.out) {
+      uint8_t *out = static_cast<uint8_t *>(p.out) + (row * p.out_stride + 8 * c) * (kWide ? 4 : 2);
+      if (kWide) {
+        reinterpret_cast<float4 *>(out)[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+        reinterpret_cast<float4 *>(out)[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+      } else {
+        *reinterpret_cast<uint4 *>(out) = pack8x2(r[i]);
+      }
     }
   }
   if (!p.y) return;
-  const float inv = 1.0f / sqrtf(block_sum(ss, s_part) / static_cast<float>(p.d) + p.eps_pre);
+  const float inv = 1.0f / sqrtf(row_sum<kWarp>(ss, s_part[1]) / static_cast<float>(p.d) + p.eps_pre);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nv) {
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * width;
+    if (c >= nv) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[i][e] *= inv;
+    if (p.w_pre) {
       float m[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[i][e] *= inv;
-      if (p.w_pre) {
-        load_f8(p.w_pre + 8 * c, m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] *= m[e];
-      }
-      *reinterpret_cast<uint4 *>(p.y + row * p.y_stride + 8 * c) = pack8x2(r[i]);
+      get8(reinterpret_cast<const float4 *>(p.w_pre) + 2 * c, m);
+      mul8(r[i], m);
     }
+    *reinterpret_cast<uint4 *>(p.y + row * p.y_stride + 8 * c) = pack8x2(r[i]);
   }
+}
+
+template <int NV, bool kWarp>
+cudaError_t launch(const BlockNormParams &p, cudaStream_t s) {
+  const int per_cta = kWarp ? kWarpRows : 1;
+  const dim3 grid(static_cast<unsigned>((p.rows + per_cta - 1) / per_cta));
+  const dim3 block(kWarp ? 32 * kWarpRows : ((p.d >> 3) + NV * 32 - 1) / (NV * 32) * 32);
+  if (p.post)
+    return p.res_fp32 ? launch_pdl(block_norm_kernel<NV, kWarp, true, true>, grid, block, 0, s, 1, p)
+                      : launch_pdl(block_norm_kernel<NV, kWarp, true, false>, grid, block, 0, s, 1, p);
+  return p.res_fp32 ? launch_pdl(block_norm_kernel<NV, kWarp, false, true>, grid, block, 0, s, 1, p)
+                    : launch_pdl(block_norm_kernel<NV, kWarp, false, false>, grid, block, 0, s, 1, p);
 }
 
 }  // namespace
 
-int launch_block_norm(const BlockNormParams &p, int64_t rows, cudaStream_t s) {
-  if (rows > 0x7FFFFFFF) return GDR_ERR_SHAPE;
-  const int nv = p.d >> 3;
-  const int threads = ((nv + kVec - 1) / kVec + 31) / 32 * 32;
-  return launch_status(launch_pdl(block_norm_kernel, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, 1, p),
-                       "block norm: kernel launch");
+int launch_block_norm(const BlockNormParams &p, cudaStream_t s) {
+  if (p.rows > 0x7FFFFFFF) return GDR_ERR_SHAPE;
+  const int d = p.d;
+  const cudaError_t e = d <= 256     ? launch<1, true>(p, s)
+                        : d <= 512   ? launch<2, true>(p, s)
+                        : d <= 1024  ? launch<4, true>(p, s)
+                        : d <= 8192  ? launch<2, false>(p, s)
+                        : d <= 16384 ? launch<4, false>(p, s)
+                                     : launch<8, false>(p, s);
+  return launch_status(e, "block norm: kernel launch");
 }
 
 }  // namespace gdr

@@ -534,6 +534,7 @@ int gdr_block_norm(const gdr_block_norm_t *a, int64_t rows, int64_t d, void *str
   if (rows == 0) return GDR_OK;
   if (!a->x || (!a->residual_out && !a->y)) return GDR_ERR_NULL;
   BlockNormParams p;
+  p.rows = rows;
   p.d = static_cast<int>(d);
   p.x_stride = a->x_stride ? a->x_stride : d;
   p.gate_stride = a->gate_shared ? 0 : (a->gate_stride ? a->gate_stride : d);
@@ -575,7 +576,7 @@ int gdr_block_norm(const gdr_block_norm_t *a, int64_t rows, int64_t d, void *str
   p.alpha = a->alpha;
   p.eps_post = a->eps_post;
   p.eps_pre = a->eps_pre;
-  return launch_block_norm(p, rows, static_cast<cudaStream_t>(stream));
+  return launch_block_norm(p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -134,10 +134,11 @@ struct BlockNormParams {
   const float *w_pre;
   uint16_t *y;
   int64_t x_stride, gate_stride, res_stride, out_stride, y_stride;
+  int64_t rows;
   int d, post, res_fp32;
   float alpha, eps_post, eps_pre;
 };
-int launch_block_norm(const BlockNormParams &p, int64_t rows, cudaStream_t s);
+int launch_block_norm(const BlockNormParams &p, cudaStream_t s);
 // y[M][N] = x[M][K] W[N][K]^T in bf16 with fp32 accumulation (linear.cu)
 int launch_linear(const void *x, const void *w, void *y, int64_t M, int64_t N, int64_t K, cudaStream_t s);
 // window schedule of a prefill call on the current device (windows, chunks per window,

@@ -459,7 +459,7 @@ def test_binding_refuses_on_the_gpu(gpu):
     cu = np.array([0, 4], np.int32)
     a = dict(q=z(4, 1, D), k=z(4, 1, D), v=z(4, 2, D), log_decay=z(2, dtype=torch.float32),
              cu_seqlens=torch.tensor(cu, device="cuda"), cu_seqlens_host=cu)
-    for name, bad in (("q", z(4, 1, 64)), ("k", z(4, 2, D)), ("q", z(3, 1, D)), ("log_decay", z(1, dtype=torch.float32)),
+    for name, bad in (("q", z(1, 1, D).expand(4, 1, D)), ("q", z(4, 1, 64)), ("k", z(4, 2, D)), ("q", z(3, 1, D)), ("log_decay", z(1, dtype=torch.float32)),
                       ("h0", z(1, 1, D, D, dtype=torch.float32)), ("hT", z(2, 2, D, D, dtype=torch.float32)),
                       ("o", z(4, 1, D)), ("cu_seqlens", torch.zeros(3, dtype=torch.int32, device="cuda"))):
         with pytest.raises(ValueError):
