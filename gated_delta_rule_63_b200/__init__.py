@@ -106,17 +106,17 @@ def lib(path: Optional[str] = None):
                                              ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
     i64 = ctypes.c_int64
     L.gdr_decay_attn_prefill.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
-                                         ctypes.c_int, _vp, _ip, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                         ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                                          _vp]
     L.gdr_decay_attn_prefill_slots.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
-                                               ctypes.c_int, _vp, _ip, ctypes.c_int, _vp, ctypes.c_int, _vp,
+                                               ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp,
                                                ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
     L.gdr_decay_attn_decode.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
                                         ctypes.c_int, _vp, _vp, ctypes.c_int, _vp]
     L.gdr_decay_attn_decode_slots.argtypes = [_vp, _vp, _vp, i64, i64, i64, _vp, ctypes.c_float, ctypes.c_int,
                                               ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp]
     L.gdr_decay_attn_prefill_workspace_size.restype = ctypes.c_size_t
-    L.gdr_decay_attn_prefill_workspace_size.argtypes = [_ip, ctypes.c_int, ctypes.c_int]
+    L.gdr_decay_attn_prefill_workspace_size.argtypes = [_vp, ctypes.c_int, ctypes.c_int]
     L.gdr_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), i64, i64, _vp]
     for fn in ("gdr_decay_attn_prefill", "gdr_decay_attn_prefill_slots", "gdr_decay_attn_decode",
                "gdr_decay_attn_decode_slots", "gdr_block_norm"):
@@ -550,7 +550,7 @@ def _decay_o(call, o, v, hv, rows):
     """o (made when None) and its pointer; it may have more rows than the call writes."""
     torch = _torch()
     if o is None:
-        o = torch.empty((v.shape[0], hv, HEAD_DIM), dtype=torch.bfloat16, device=v.device)
+        o = torch.empty_like(v)   # v's shape, dense (v has dense rows)
         return o, o.data_ptr()
     if isinstance(o, torch.Tensor) and (o.dim() != 3 or o.shape[0] < rows):
         raise ValueError(f"o must be [{rows}, {hv}, {HEAD_DIM}], got {tuple(o.shape)}")
@@ -560,22 +560,25 @@ def _decay_o(call, o, v, hv, rows):
 def decay_attn_workspace(cu_seqlens_host, hv: int, device):
     """A torch uint8 device buffer sized for gdr_decay_attn_prefill, or None when it needs none."""
     torch = _torch()
-    cu, cup = _host_cu(cu_seqlens_host)
-    nbytes = int(lib().gdr_decay_attn_prefill_workspace_size(cup, cu.shape[0] - 1, int(hv)))
+    cu, _ = _host_cu(cu_seqlens_host)
+    nbytes = int(lib().gdr_decay_attn_prefill_workspace_size(cu.ctypes.data, cu.shape[0] - 1, int(hv)))
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _decay_prefill(name, q, k, v, log_decay, cu_seqlens, cu_seqlens_host, states, o, scale, workspace, stream):
     """The prefill call `name`; states(call, n, hv) gives its arguments between n_seqs and o."""
     torch = _torch()
-    cu, cup = _host_cu(cu_seqlens_host)
+    cu = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
+    cup = cu.ctypes.data
     if cu.ndim != 1 or cu.shape[0] < 1:
         raise ValueError("cu_seqlens_host must hold n_seqs + 1 offsets")
     n, total = cu.shape[0] - 1, int(cu[-1])
     call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, total)
     o, op = _decay_o(call, o, v, hv, total)
     if workspace is None:
-        workspace = decay_attn_workspace(cu, hv, v.device)
+        need = lib().gdr_decay_attn_prefill_workspace_size(cup, n, hv)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
     wp, wbytes = (None, 0) if workspace is None else (
         call.dense(workspace, torch.uint8, "workspace", workspace.shape), workspace.numel())
     call.run(name, getattr(lib(), name), stream, *ins, float(scale), hk, hv,
@@ -655,12 +658,12 @@ def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None
     d = int(x.shape[-1]) if x.dim() else 0
     rows = x.numel() // d if d else 0
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else bf
-    if rdt != bf and rdt != f32:
+    if rdt is not bf and rdt is not f32:
         raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {rdt}")
     if residual_out is None and want_residual:
-        residual_out = torch.empty(x.shape, dtype=rdt, device=x.device)
+        residual_out = torch.empty_like(x) if rdt is bf else torch.empty_like(x, dtype=f32)
     if y is None and want_y:
-        y = torch.empty(x.shape, dtype=bf, device=x.device)
+        y = torch.empty_like(x)
     shared = gate is not None and gate.dim() == 1
     xp, xs = call.rows(x, bf, "x", rows, d)
     gp, gs = call.rows(gate, bf, "gate", 1 if shared else rows, d)
