@@ -32,15 +32,15 @@
 //                a branch of lane 0 each product took 76 to 117 cycles of issuing alone.
 // The handoffs are mbarriers (what completes it -> what it allows):
 //   full[s]      the copies of a chunk landed -> the products may read them, V' may be made
-//   empty[s]     the chunk's last product is done -> its stage may be refilled
+//   empty[s]     the chunk's last product is done -> its stage may be refilled (arrived at by a warp
+//                that waits for that product: a commit holds the issuing lane for some 130 cycles)
 //   vt[]         V' of chunk c is in TMEM, a partial chunk's tail rows are zero -> KV(c), S(c)
 //   kv[]         KV(c) is done -> the state takes it, V' may be rewritten
 //   kv_free      the state has read KV(c) -> KV(c + 1) may overwrite it
 //   s            S(c) is done -> P(c)
 //   h            H before chunk c is in TMEM -> OI(c)
-//   oi           OI(c) is done -> H may be rewritten
 //   p            P(c) is in shared memory -> PV(c)
-//   o            PV(c) is done, and with it all of chunk c -> o(c), P may be rewritten
+//   o            PV(c) is done, and with it all of chunk c -> o(c), H and P may be rewritten
 //   o_free       o(c) is out of TMEM -> S(c + 1), OI(c + 1)
 // S and PV share their columns: P(c), which PV(c) waits for, is made from S(c).
 // No barrier runs two phases ahead of a waiter: each arrival for chunk c + 1 comes after a
@@ -324,7 +324,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint8_t *smem = smem_raw + (sbase - raw_addr);
   volatile uint8_t *bad = smem + OFF_BAD;
   const uint32_t b_full = sbase + OFF_BAR, b_empty = b_full + 8 * kStages, b_vt = b_empty + 8 * kStages;
-  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_kv_free = b_kv + 24, b_h = b_kv + 32, b_oi = b_kv + 40,
+  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_kv_free = b_kv + 24, b_h = b_kv + 32,
                  b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
   constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 10);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + OFF_BAR + kWords);
@@ -343,7 +343,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(b_s, 1);
     mbar_init(b_kv_free, 8);
     mbar_init(b_h, 8);
-    mbar_init(b_oi, 1);
     mbar_init(b_p, 4);
     mbar_init(b_o, 1);
     mbar_init(b_o_free, 4);
@@ -461,7 +460,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             mma_bf16_ts(kv, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), idesc_bf16(128, 128, false, true),
                         term < 2 || kk > 0);
         mma_commit(kv_bar(c));
-        if (!kOut) mma_commit(b_empty + 8 * s);
       }
       __syncwarp();
       if (!kOut) {
@@ -491,7 +489,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8, aq + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
                         idesc_bf16(128, 64, false, false), part < 1 || kk > 0);
-        mma_commit(b_oi);
       }
       __syncwarp();
       if (!wait_warp(b_p, c)) break;
@@ -506,7 +503,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), dp + ((part * HALF + kk * 32) >> 4),
                      idesc_bf16(128, 64, true, false), part < 1 || kk > 0);
         mma_commit(b_o);
-        mma_commit(b_empty + 8 * s);
       }
       __syncwarp();
       go = c + 1 == n_chunks || kv_ready(c + 1);
@@ -578,6 +574,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (c > 0) bulk_wait_read();   // o(c - 1) has left its tile
         }
         if (!wait_warp(b_o, c)) break;
+        if (warp == 0 && lane == 0) mbar_arrive(b_empty + 8 * (c % kStages));
         tc_fence_after();
         // a value that was not finite reaches every later row of its dv (see warps 4..11)
         volatile uint8_t *mark = bad + (c & 3) * 2 * D + 32 * warp + lane;
@@ -791,7 +788,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (more) finish_vt(c + 1);
         take_kv(c);
         if (more) {
-          if (!(go = wait_warp(b_oi, c))) break;
+          if (!(go = wait_warp(b_o, c))) break;   // (OI(c) is done with the H before)
           tc_fence_after();
           put_h();
         }
@@ -808,6 +805,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         vt_made(c);
         if (c > 0) {
           if (!(go = kv_done(c - 1))) break;
+          if (warp == 4 && lane == 0) mbar_arrive(b_empty + 8 * ((c - 1) % kStages));
           take_kv(c - 1);
         }
       }
