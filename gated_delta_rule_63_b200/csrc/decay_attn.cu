@@ -101,8 +101,12 @@ struct DecayPrefillParams {
   float scale;
   int hv, group, n_seqs;
   int seg_chunks;      // chunks of a segment; 0: every sequence is one unit
+  int early;           // segments that are not their sequence's last
+  int piece_chunks, pieces;   // parts of such a segment in the state-only launch
   DecayStates st;
-  float *ws;           // [segments][hv][D][D]: what segments add; a sequence's last: its initial state
+  // [slots][hv][D][D]: for each sequence in turn its initial state and what each piece of its early
+  // segments adds
+  float *ws;
   uint16_t *o;
   int *err;
   // Up to kListed sequences: where each begins and ends, the longest first (a launch then ends with
@@ -289,26 +293,33 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
 }
 
 // Which part of which sequence a unit is.  Units are the segments of the listed sequences in turn
-// (a sequence without tokens is one), in the state-only launch without each sequence's last.
+// (a sequence without tokens is one); in the state-only launch the first pieces of the early
+// segments in turn, then their second ones, and so on (the last, shorter ones at the end).
 struct Unit {
-  int seq, seg, segs;
-  int first;          // number of the sequence's first segment
+  int seq, seg, segs, piece;
+  int slot;           // of the sequence's initial state; segment s's pieces are from 1 + s * pieces on
   int t_begin, t_end;
 };
 template <bool kOut>
 __device__ __forceinline__ Unit find_unit(const DecayPrefillParams &p, int unit) {
-  if (p.n_seqs > kListed) return Unit{unit, 0, 1, unit, p.cu[unit], p.cu[unit + 1]};
-  if (p.seg_chunks == 0) return Unit{p.seq[unit], 0, 1, unit, p.begin[unit], p.end[unit]};
+  if (p.n_seqs > kListed) return Unit{unit, 0, 1, 0, 0, p.cu[unit], p.cu[unit + 1]};
+  if (p.seg_chunks == 0) return Unit{p.seq[unit], 0, 1, 0, 0, p.begin[unit], p.end[unit]};
+  Unit u;
+  u.piece = kOut ? 0 : unit / p.early;
+  if (!kOut) unit -= u.piece * p.early;
   int i = 0;   // the last one whose first unit is not behind this one
   while (i + 1 < p.n_seqs && unit >= p.first[i + 1] - (kOut ? 0 : i + 1)) ++i;
-  Unit u;
   u.seq = p.seq[i];
-  u.first = p.first[i];
-  u.seg = unit - (u.first - (kOut ? 0 : i));
+  u.seg = unit - (p.first[i] - (kOut ? 0 : i));
+  u.slot = (p.first[i] - i) * p.pieces + i;
   const int chunks = (p.end[i] - p.begin[i] + C - 1) / C;
   u.segs = max(1, (chunks + p.seg_chunks - 1) / p.seg_chunks);
   u.t_begin = p.begin[i] + u.seg * p.seg_chunks * C;
   u.t_end = u.seg == u.segs - 1 ? p.end[i] : u.t_begin + p.seg_chunks * C;
+  if (!kOut) {
+    u.t_begin += u.piece * p.piece_chunks * C;
+    u.t_end = min(u.t_end, u.t_begin + p.piece_chunks * C);
+  }
   return u;
 }
 
@@ -378,8 +389,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   float *state_out;
   p.st.resolve(un.seq, h, p.hv, &state_in, &state_out);
   constexpr int64_t kState = static_cast<int64_t>(D) * D;
-  // a sequence's segments lie one behind the other in the workspace
-  float *ws = p.ws + (static_cast<int64_t>(un.first) * p.hv + h) * kState;
+  float *ws = p.ws + (static_cast<int64_t>(un.slot) * p.hv + h) * kState;
   const int64_t ws_step = p.hv * kState;
 
   const auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
@@ -663,33 +673,34 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     };
     const auto load_h = [&]() {
       const int64_t at = static_cast<int64_t>(64 * half) * D + dv;
-      if (un.seg == 0) {
+      if (un.seg == 0 && un.piece == 0) {
         // (a split sequence's second launch reads the copy: another CTA may write state_out meanwhile)
-        const float *src = state_in == nullptr ? nullptr
-                           : (kOut && un.segs > 1) ? ws + (un.segs - 1) * ws_step
-                                                   : state_in;
+        const float *src = state_in == nullptr ? nullptr : kOut && un.segs > 1 ? ws : state_in;
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           H[e] = src ? make_float2(src[at + 2 * e * D], src[at + (2 * e + 1) * D]) : make_float2(0.0f, 0.0f);
         if (!kOut && src) {
-          float *copy = ws + (un.segs - 1) * ws_step + at;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            copy[2 * e * D] = H[e].x;
-            copy[(2 * e + 1) * D] = H[e].y;
+            ws[at + 2 * e * D] = H[e].x;
+            ws[at + (2 * e + 1) * D] = H[e].y;
           }
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) H[e] = make_float2(0.0f, 0.0f);
-        if (kOut) {   // the segments before this one, each decayed over those after it
-          const DecayStep step = decay_step(g, static_cast<int64_t>(p.seg_chunks) * C);
-          for (int j = 0; j < un.seg; ++j) {
-            const float *src = ws + j * ws_step + at;
+        if (kOut) {   // the pieces before this segment, each decayed over those after it
+          const DecayStep piece = decay_step(g, static_cast<int64_t>(p.piece_chunks) * C);
+          const DecayStep rest =
+              decay_step(g, static_cast<int64_t>(p.seg_chunks - (p.pieces - 1) * p.piece_chunks) * C);
+          const float *src = ws + ws_step + at;
+          for (int j = 0; j < un.seg; ++j)
+            for (int i = 0; i < p.pieces; ++i, src += ws_step) {
+              const DecayStep step = i + 1 < p.pieces ? piece : rest;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              H[e] = step.apply2(H[e], make_float2(src[2 * e * D], src[(2 * e + 1) * D]));
-          }
+              for (int e = 0; e < 32; ++e)
+                H[e] = step.apply2(H[e], make_float2(src[2 * e * D], src[(2 * e + 1) * D]));
+            }
         }
       }
     };
@@ -811,7 +822,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       if (n_chunks > 0 && go && (go = kv_done(n_chunks - 1))) take_kv(n_chunks - 1);
     }
-    float *dst = !kOut ? ws + un.seg * ws_step : un.seg == un.segs - 1 ? state_out : nullptr;
+    float *dst = !kOut ? ws + (1 + un.seg * p.pieces + un.piece) * ws_step : un.seg == un.segs - 1 ? state_out : nullptr;
     if (go && dst) {
       dst += static_cast<int64_t>(64 * half) * D + dv;
 #pragma unroll
@@ -826,18 +837,21 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (warp == 13) tmem_dealloc(tmem, TC_ALL);
 }
 
-// Chunks of a segment (0: no sequence is split) and the number of units.
+// How a call's sequences are cut: into segments of seg_chunks chunks (0: not at all), every segment
+// but a sequence's last into pieces for the state-only launch.
 struct DecayPlan {
   int seg_chunks;
-  int units;   // segments
-  int early;   // segments that are not their sequence's last
+  int units;                  // segments
+  int early;                  // those that are not their sequence's last
+  int piece_chunks, pieces;
+  int slots;                  // states in the workspace
 };
 
 // How long a launch takes whose units (count heads x a length in chunks each, the longest first) go
 // to 148 SMs, one at a time on each, the next one to the SM that is free first.
 struct Launch {
-  double at[kMostSplit * 32 + 1];   // SMs by the time they are free, ascending
-  int sms[kMostSplit * 32 + 1];
+  double at[kSms + 1];   // SMs by the time they are free, ascending; one of them at least for each time
+  int sms[kSms + 1];
   int n;
   Launch() : n(1) { at[0] = 0.0, sms[0] = kSms; }
   void add(int units, double chunks) {
@@ -870,9 +884,9 @@ int chunks_of(const int32_t *cu, int n) {
 
 // Splitting pays when few (sequence, head) units leave SMs idle.  Times in chunks of the main launch
 // (3200 cycles): the state-only launch takes 0.42 of one for each of its chunks, and a split costs
-// another launch (4) and the earlier segments' states for each segment (0.6 for each).
+// another launch (4) and the pieces' states for each later segment (0.6 for each).
 DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
-  DecayPlan best{0, n_seqs, 0};
+  DecayPlan best{0, n_seqs, 0, 0, 0, 0};
   if (n_seqs > kMostSplit || static_cast<int64_t>(n_seqs) * hv > 2 * kSms) return best;
   int nc[kMostSplit];
   for (int n = 0; n < n_seqs; ++n) nc[n] = chunks_of(cu, n);
@@ -880,20 +894,29 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
   Launch whole;
   for (int n = 0; n < n_seqs; ++n) whole.add(hv, nc[n]);
   double least = whole.time();
+  int64_t load = 0;
+  for (int n = 0; n < n_seqs; ++n) load += static_cast<int64_t>(nc[n]) * hv;
+  if (least <= 1.1 * static_cast<double>(load) / kSms) return best;   // no SM is idle for long
   for (int s = 2; s <= 32; ++s) {
     const int len = (nc[0] + s - 1) / s;
     if (len < 4) break;
-    Launch main, early;
-    int units = 0, split = 0;
+    int units = 0;
     for (int n = 0; n < n_seqs; ++n) units += std::max(1, (nc[n] + len - 1) / len);
-    split = units - n_seqs;
+    const int split = units - n_seqs;
+    Launch main;
     main.add(split * hv, len);
-    early.add(split * hv, 0.42 * len);
     for (int n = 0; n < n_seqs; ++n) main.add(hv, nc[n] > 0 ? (nc[n] - 1) % len + 1 : 0);
-    const double t = main.time() + early.time() + 4.0 + 0.6 * (s - 1);
-    if (t < least) {
-      least = t;
-      best = DecayPlan{len, units, split};
+    const double base = main.time() + 4.0;
+    // a whole segment on each SM, or two thirds and a third (two thirds of the SMs, then all)
+    for (int part : {len, (2 * len + 2) / 3}) {
+      const int pieces = (len + part - 1) / part;
+      Launch state;
+      for (int i = 0; i < pieces; ++i) state.add(split * hv, 0.42 * std::min(part, len - i * part));
+      const double t = base + state.time() + 0.6 * pieces * (s - 1);
+      if (t < least) {
+        least = t;
+        best = DecayPlan{len, units, split, part, pieces, split * pieces + n_seqs};
+      }
     }
   }
   return best;
@@ -914,7 +937,7 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, ui
 
 size_t decay_prefill_workspace_bytes(const int32_t *cu, int n_seqs, int hv) {
   const DecayPlan plan = plan_decay(cu, n_seqs, hv);
-  return plan.seg_chunks == 0 ? 0 : static_cast<size_t>(plan.units) * hv * D * D * sizeof(float);
+  return plan.seg_chunks == 0 ? 0 : static_cast<size_t>(plan.slots) * hv * D * D * sizeof(float);
 }
 
 int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
@@ -936,7 +959,7 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   if (!tensor_map_encoder())
     return launch_status(cudaErrorSymbolNotFound, "decay prefill: cuTensorMapEncodeTiled lookup");
   const DecayPlan plan = plan_decay(cu_host, n_seqs, hv);
-  if (plan.units > 65535) return GDR_ERR_SHAPE;
+  if (plan.units > 65535) return GDR_ERR_SHAPE;   // (a grid's second dimension)
   // without a token nothing is copied; the maps still need an address
   const bool any = cu_host[n_seqs] > 0;
   const void *none = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(cu_dev) & ~uintptr_t{15});
@@ -956,6 +979,9 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   p.group = hv / hk;
   p.n_seqs = n_seqs;
   p.seg_chunks = plan.seg_chunks;
+  p.early = plan.early;
+  p.piece_chunks = plan.piece_chunks;
+  p.pieces = plan.pieces;
   if (n_seqs <= kListed) {
     // (eight prompts of 1 to 7777 tokens, the longest the sixth: 437 us in their own order, 317 us so)
     for (int n = 0; n < n_seqs; ++n) p.seq[n] = static_cast<uint8_t>(n);
@@ -976,7 +1002,7 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   p.o = static_cast<uint16_t *>(o);
   p.err = device_error_ptr();
   if (plan.seg_chunks != 0) {
-    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, dim3(hv, plan.early), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
+    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, dim3(hv, plan.early * plan.pieces), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
                                  "decay prefill: segment kernel launch");
     if (st) return st;
   }

@@ -66,6 +66,32 @@ def bounds(q, k, v, g, cu, h0, scale):
     return scale * A, scale * Bo, Habs
 
 
+def in_chunks(q, k, v, g, cu, h0, scale):
+    """The chunked form in fp64 (torch tensors, hk = hv): o, H and the A, B, Habs of the bounds."""
+    n, hv = len(cu) - 1, v.shape[1]
+    o, A, Bo = torch.zeros_like(v), torch.zeros_like(v), torch.zeros_like(v)
+    H = torch.zeros(n, hv, D, D, dtype=v.dtype, device=v.device) if h0 is None else h0.clone()
+    Habs = H.abs()
+    for s in range(n):
+        for a in range(int(cu[s]), int(cu[s + 1]), CH):
+            b = min(a + CH, int(cu[s + 1]))
+            x, y, z = (w[a:b].transpose(0, 1) for w in (q, k, v))          # [hv, m, D]
+            i = torch.arange(b - a, device=v.device)
+            low = (i[:, None] >= i).to(v.dtype)
+            w = (g[:, None, None] * (i[:, None] - i).clamp(min=0)).exp() * low
+            to_here = (g[:, None] * (i + 1)).exp()[..., None]
+            to_end = (g[:, None] * (b - a - 1 - i)).exp()[..., None]
+            P = x @ y.transpose(1, 2) * w
+            o[a:b] = scale * (to_here * (x @ H[s]) + P @ z).transpose(0, 1)
+            A[a:b] = scale * (to_here * (x.abs() @ H[s].abs()) + P.abs() @ z.abs()).transpose(0, 1)
+            Bo[a:b] = scale * (to_here * (x.abs() @ Habs[s])
+                               + (x.abs() @ y.abs().transpose(1, 2) * w) @ z.abs()).transpose(0, 1)
+            last = (g * (b - a)).exp()[:, None, None]
+            H[s] = last * H[s] + (y * to_end).transpose(1, 2) @ z
+            Habs[s] = last * Habs[s] + (y.abs() * to_end).transpose(1, 2) @ z.abs()
+    return o, H, A, Bo, Habs
+
+
 def dev(x, dtype=torch.bfloat16):
     return torch.tensor(np.asarray(x, np.float64), dtype=torch.float64).to("cuda").to(dtype)
 
@@ -133,6 +159,17 @@ def test_oracle_split_and_packed():
         o1, H1 = O.decay_attn(q[a:m], k[a:m], v[a:m], g, [0, m - a], h0[n:n + 1])
         o2, H2 = O.decay_attn(q[m:b], k[m:b], v[m:b], g, [0, b - m], H1)
         assert np.array_equal(np.concatenate([o1, o2]), o[a:b]) and np.array_equal(H2[0], H[n])
+
+
+def test_oracle_equals_the_chunked_form():
+    """The chunked form in fp64, and the magnitudes of the bounds, on sequences around chunk borders."""
+    q, k, v, cu, h0 = make(4, [130, 0, 64, 1], 2, 2, 1.0)
+    g = np.array([-0.3, -1e-4])
+    o, H = O.decay_attn(q, k, v, g, cu, h0, 0.7)
+    A, Bo, Habs = bounds(q, k, v, g, cu, h0, 0.7)
+    got = in_chunks(*(torch.tensor(x) for x in (q, k, v, g)), cu, torch.tensor(h0).double(), 0.7)
+    for x, want in zip(got, (o, H, A, Bo, Habs)):
+        assert np.allclose(x.numpy(), want, rtol=1e-10, atol=1e-10)
 
 
 # ---------------------------------------------------------------------------
@@ -277,6 +314,41 @@ def test_prefill_matches_oracle(gpu, lengths, hk, hv, h0_std, kind, views):
          "grow": 1e-3 * (1 + np.arange(hv))}[kind].astype(np.float32)
     o, hT = run(q, k, v, g, cu, h0, scale=D ** -0.5, views=views)
     check(o, hT, q, k, v, g, cu, h0, D ** -0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_seqs", [33, 65, 90])
+def test_prefill_of_many_sequences(gpu, n_seqs):
+    """More sequences than are ever split, and more than ride in the launch parameters."""
+    lengths = [int(x) for x in np.random.default_rng(n_seqs).integers(0, 70, n_seqs)]
+    q, k, v, cu, h0 = make(12, lengths, 1, 1, 1.0)
+    g = np.array([-0.02], np.float32)
+    o, hT = run(q, k, v, g, cu, h0, scale=0.5)
+    check(o, hT, q, k, v, g, cu, h0, 0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,hv,h0_std", [([64 * 40], 48, None), ([64 * 37 + 5, 1, 0, 700], 16, 1.0),
+                                               ([5000], 4, 1.0), ([9000, 100], 3, None)])
+def test_prefill_in_segments(gpu, lengths, hv, h0_std):
+    """Long sequences of few heads, which run as segments beside each other."""
+    rng = np.random.default_rng(3)
+    T, n = sum(lengths), len(lengths)
+    t = lambda *s: torch.tensor(rng.standard_normal(s), device="cuda").to(torch.bfloat16)   # noqa: E731
+    q, k, v = t(T, hv, D), t(T, hv, D), t(T, hv, D)
+    g = torch.tensor(slopes(hv), device="cuda")
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    assert G.decay_attn_workspace(cu, hv, "cuda") is not None    # (split indeed)
+    h0 = None if h0_std is None else torch.tensor(h0_std * rng.standard_normal((n, hv, D, D)), dtype=torch.float32,
+                                                  device="cuda")
+    ref_o, ref_h, A, Bo, Habs = in_chunks(q.double(), k.double(), v.double(), g.double(), cu,
+                                          None if h0 is None else h0.double(), 0.1)
+    hT = torch.empty(n, hv, D, D, device="cuda") if h0 is None else h0
+    o = G.decay_attn_prefill(q, k, v, g, torch.tensor(cu, device="cuda"), cu, h0=h0, hT=hT, scale=0.1)
+    assert bool(((o.double() - ref_o).abs() <= U * ref_o.abs() * (1 + U) + 2 * U * U * A + 256 * E * Bo).all())
+    for i, x in enumerate(lengths):
+        bound = (64 + 16 + 2 * ((x + CH - 1) // CH)) * E * Habs[i]
+        assert bool(((hT[i].double() - ref_h[i]).abs() <= bound).all())
 
 
 @pytest.mark.gpu
