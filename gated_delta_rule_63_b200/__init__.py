@@ -534,6 +534,16 @@ class _Call:
             raise GdrError(name, code)
 
 
+def _on_stream(stream, make):
+    """make() with the tensors it makes belonging to the call's stream: given back to the allocator
+    (a workspace at the end of the call), their memory is then not used before the call's kernels
+    are through with it."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
+
+
 def _decay_inputs(q, k, v, log_decay, rows):
     """The call and the checked arguments the decayed linear attention calls share, in the ABI's order."""
     call = _Call(q, "q")
@@ -546,11 +556,11 @@ def _decay_inputs(q, k, v, log_decay, rows):
     return call, (qp, kp, vp, qs, ks, vs, call.dense(log_decay, _torch().float32, "log_decay", (hv,))), hk, hv
 
 
-def _decay_o(call, o, v, hv, rows):
+def _decay_o(call, o, v, hv, rows, stream):
     """o (made when None) and its pointer; it may have more rows than the call writes."""
     torch = _torch()
     if o is None:
-        o = torch.empty_like(v)   # v's shape, dense (v has dense rows)
+        o = _on_stream(stream, lambda: torch.empty_like(v))   # v's shape, dense (v has dense rows)
         return o, o.data_ptr()
     if isinstance(o, torch.Tensor) and (o.dim() != 3 or o.shape[0] < rows):
         raise ValueError(f"o must be [{rows}, {hv}, {HEAD_DIM}], got {tuple(o.shape)}")
@@ -574,11 +584,11 @@ def _decay_prefill(name, q, k, v, log_decay, cu_seqlens, cu_seqlens_host, states
         raise ValueError("cu_seqlens_host must hold n_seqs + 1 offsets")
     n, total = cu.shape[0] - 1, int(cu[-1])
     call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, total)
-    o, op = _decay_o(call, o, v, hv, total)
+    o, op = _decay_o(call, o, v, hv, total, stream)
     if workspace is None:
         need = lib().gdr_decay_attn_prefill_workspace_size(cup, n, hv)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+            workspace = _on_stream(stream, lambda: torch.empty(need, dtype=torch.uint8, device=v.device))
     wp, wbytes = (None, 0) if workspace is None else (
         call.dense(workspace, torch.uint8, "workspace", workspace.shape), workspace.numel())
     call.run(name, getattr(lib(), name), stream, *ins, float(scale), hk, hv,
@@ -592,8 +602,8 @@ def decay_attn_prefill(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, h0=None,
     o_t = scale H_t^T q_t.  q, k [T, hk, 128], v [T, hv, 128] bf16 (token-strided views allowed),
     log_decay [hv] fp32.  Returns o [T, hv, 128] bf16 (and writes hT [N, hv, 128, 128] fp32 when
     given); rows of o behind the last sequence are left as they were.  Without a workspace one is
-    made for the call when it needs one (decay_attn_workspace); a captured graph, or calls on
-    several streams, should each be given their own."""
+    made for the call when it needs one (decay_attn_workspace); calls that may run at the same time
+    must not share one."""
     f32 = _torch().float32
 
     def states(call, n, hv):
@@ -624,7 +634,7 @@ def decay_attn_decode(q, k, v, log_decay, state, o=None, scale: float = 1.0, str
     v [B, hv, 128] bf16, state [B, hv, 128, 128] fp32 updated in place -> o [B, hv, 128] bf16."""
     B = int(v.shape[0])
     call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
-    o, op = _decay_o(call, o, v, hv, B)
+    o, op = _decay_o(call, o, v, hv, B, stream)
     call.run("gdr_decay_attn_decode", lib().gdr_decay_attn_decode, stream, *ins, float(scale), hk, hv,
              call.dense(state, _torch().float32, "state", (B, hv, HEAD_DIM, HEAD_DIM)), op, B)
     return o
@@ -636,7 +646,7 @@ def decay_attn_decode_slots(q, k, v, log_decay, state_pool, slot, o=None, scale:
     torch = _torch()
     B, n_slots = int(v.shape[0]), int(state_pool.shape[0])
     call, ins, hk, hv = _decay_inputs(q, k, v, log_decay, B)
-    o, op = _decay_o(call, o, v, hv, B)
+    o, op = _decay_o(call, o, v, hv, B, stream)
     call.run("gdr_decay_attn_decode_slots", lib().gdr_decay_attn_decode_slots, stream, *ins, float(scale), hk, hv,
              call.dense(state_pool, torch.float32, "state_pool", (n_slots, hv, HEAD_DIM, HEAD_DIM)), n_slots,
              call.dense(slot, torch.int32, "slot", (B,)), op, B)
@@ -661,9 +671,9 @@ def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None
     if rdt is not bf and rdt is not f32:
         raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {rdt}")
     if residual_out is None and want_residual:
-        residual_out = torch.empty_like(x) if rdt is bf else torch.empty_like(x, dtype=f32)
+        residual_out = _on_stream(stream, lambda: torch.empty_like(x, dtype=rdt))
     if y is None and want_y:
-        y = torch.empty_like(x)
+        y = _on_stream(stream, lambda: torch.empty_like(x))
     shared = gate is not None and gate.dim() == 1
     xp, xs = call.rows(x, bf, "x", rows, d)
     gp, gs = call.rows(gate, bf, "gate", 1 if shared else rows, d)

@@ -18,10 +18,17 @@
 // far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the state stays an
 // fp32 sum (two terms would leave it an error of about 2.7e-6, ten times that of fp32 sums).
 //
-// What bounds a chunk is shared memory: MMA operands, copies and the tiles that are written
-// for them.  V' and H0 are therefore A operands in tensor memory, written from registers.
+// V' and H0 are A operands in tensor memory, written from registers: as shared-memory tiles they
+// took the bandwidth that the products read their operands with (149 -> 92 us for a prompt of 4096
+// tokens and 48 value heads, with o and V going through 8 x 8 transposes).
 //
-// One CTA (14 warps) walks the chunks of one (value head, sequence or segment of one):
+// What bounds it: the products of a chunk, 13.6 MFLOP (44 MMAs), keep the tensor pipe for about
+// 2900 of a chunk's 3150 cycles (an M = 128, N = 64, K = 16 product with A in tensor memory
+// takes 70 cycles, N = 128 79).  32 768 tokens of 48 value heads take 461 us: 0.9 PFLOP/s of such
+// products with those of the segments' states, 1.08 GB read and written once at 2.3 TB/s; a
+// prompt of 4096 tokens 69 us.  The GPU then runs at its power cap, at about 1.6 GHz.
+//
+// One CTA (16 warps, the last two idle) walks the chunks of one (value head, sequence or segment):
 //   warps 0..3   P from S (TMEM -> registers -> shared memory), and o from OI and PV
 //   warps 4..11  V' (shared memory -> TMEM), the state H in registers (thread = one dv row,
 //                64 of its dk columns), H's bf16 terms (-> TMEM)
@@ -50,7 +57,9 @@
 // Few heads and sequences leave SMs idle, so long sequences are then cut into segments that
 // run beside each other: a first launch (kOut = false: K and V only) leaves what each segment
 // but the last adds to the state, a second one starts every segment from the decayed sum of
-// those before it.  plan_decay() weighs the extra pass against the shorter chain.
+// those before it.  plan_decay() weighs the extra pass against the shorter chain; measured, in
+// one piece and as it chooses: 512 tokens of 48 value heads 19.7 (not cut), 1024 33.2 and 27.4,
+// 4096 114 and 68.5, 16 384 437 and 228 us; 4096 of 16 heads 113 and 42.6, 8192 of 2 219 and 41 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -68,9 +77,11 @@ namespace {
 constexpr int D = kHeadDim;
 constexpr int C = kChunk;            // tokens of a chunk
 constexpr int kThreads = 512;
-// registers a thread: 128 at launch (512 x 128 is the whole file); warps 12..15 give up theirs for
-// the state's: 128 x 56 + 128 x 128 + 256 x 160 = 64512 of 65536
-constexpr int kRegsFew = 56, kRegsState = 168, kRegsOut = 120;
+// Registers a thread.  512 threads have 128 each at launch, the whole file; warps 12..15 and 0..3 give
+// some of theirs to the state's warps, which spilled 740 bytes without (107 instead of 81 us for a
+// prompt of 4096 tokens).  The launcher checks that the launch has them to give.
+constexpr int kRegsLaunch = 128, kRegsFew = 56, kRegsOut = 120, kRegsState = 168;
+static_assert(128 * kRegsFew + 128 * kRegsOut + 256 * kRegsState <= kThreads * kRegsLaunch, "register split");
 constexpr int kStages = 4;
 constexpr int kSms = 148;
 
@@ -416,113 +427,113 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   };
 
   if (warp >= 12) {
-   regs_dec<kRegsFew>();
-   if (warp == 12) {
-    if (lane == 0) {
-      // ---- copies: chunk c into a stage once the products of the chunk before it there are done
-      const int qk_col = (h / p.group) * D, v_col = h * D;
-      int issued = 0;
-      for (int c = 0; c < n_chunks; ++c) {
+    regs_dec<kRegsFew>();
+    if (warp == 12) {
+      if (lane == 0) {
+        // ---- copies: chunk c into a stage once the products of the chunk before it there are done
+        const int qk_col = (h / p.group) * D, v_col = h * D;
+        int issued = 0;
+        for (int c = 0; c < n_chunks; ++c) {
+          const int s = c % kStages;
+          if (c >= kStages && !wait(b_empty + 8 * s, (c / kStages) - 1)) break;
+          const uint32_t st = sbase + s * STAGE, full = b_full + 8 * s;
+          const int t0 = t_begin + c * C;
+          mbar_arrive_expect_tx(full, kOut ? STAGE : 2 * TILE);
+          tma_load_2d(st + OFF_V, &tm_v, v_col, t0, full);
+          tma_load_2d(st + OFF_V + HALF, &tm_v, v_col + 64, t0, full);
+          tma_load_2d(st + OFF_K, &tm_k, qk_col, t0, full);
+          tma_load_2d(st + OFF_K + HALF, &tm_k, qk_col + 64, t0, full);
+          if (kOut) {
+            tma_load_2d(st + OFF_Q, &tm_q, qk_col, t0, full);
+            tma_load_2d(st + OFF_Q + HALF, &tm_q, qk_col + 64, t0, full);
+          }
+          issued = c + 1;
+        }
+        // after a timeout elsewhere the copies in flight land before the CTA leaves
+        for (int c = (issued > kStages ? issued - kStages : 0); c < issued; ++c)
+          mbar_wait(b_full + 8 * (c % kStages), (c / kStages) & 1, p.err, 1u << 16);
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---- products
+      const bool elected = elect_one();
+      // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
+      const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
+      const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
+      const uint64_t dp = sdesc(sbase + OFF_P, 16, 1024);
+      const auto kv_ready = [&](int c) {   // KV(c) may be issued
+        return landed(c) && wait_warp(vt_bar(c), phase2(c)) &&
+               (!kOut || c == 0 || wait_warp(b_kv_free, c - 1));
+      };
+      bool go = n_chunks > 0 && kv_ready(0);
+      for (int c = 0; c < n_chunks && go; ++c) {
         const int s = c % kStages;
-        if (c >= kStages && !wait(b_empty + 8 * s, (c / kStages) - 1)) break;
-        const uint32_t st = sbase + s * STAGE, full = b_full + 8 * s;
-        const int t0 = t_begin + c * C;
-        mbar_arrive_expect_tx(full, kOut ? STAGE : 2 * TILE);
-        tma_load_2d(st + OFF_V, &tm_v, v_col, t0, full);
-        tma_load_2d(st + OFF_V + HALF, &tm_v, v_col + 64, t0, full);
-        tma_load_2d(st + OFF_K, &tm_k, qk_col, t0, full);
-        tma_load_2d(st + OFF_K + HALF, &tm_k, qk_col + 64, t0, full);
-        if (kOut) {
-          tma_load_2d(st + OFF_Q, &tm_q, qk_col, t0, full);
-          tma_load_2d(st + OFF_Q + HALF, &tm_q, qk_col + 64, t0, full);
+        const uint64_t st = static_cast<uint64_t>(s * STAGE) >> 4;
+        tc_fence_after();
+        const uint32_t kv = kv_col(c), vt = vt_col(c);
+        const uint64_t bk = dk_mn0 + st, aq = dq0 + st;
+        if (elected) {
+          // KV(c) = V'^T K, the smallest terms first
+#pragma unroll
+          for (int term = 2; term >= 0; --term)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(kv, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), idesc_bf16(128, 128, false, true),
+                          term < 2 || kk > 0);
+          mma_commit(kv_bar(c));
         }
-        issued = c + 1;
-      }
-      // after a timeout elsewhere the copies in flight land before the CTA leaves
-      for (int c = (issued > kStages ? issued - kStages : 0); c < issued; ++c)
-        mbar_wait(b_full + 8 * (c % kStages), (c / kStages) & 1, p.err, 1u << 16);
-    }
-    __syncwarp();
-   } else if (warp == 13) {
-    // ---- products
-    const bool elected = elect_one();
-    // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
-    const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
-    const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
-    const uint64_t dp = sdesc(sbase + OFF_P, 16, 1024);
-    const auto kv_ready = [&](int c) {   // KV(c) may be issued
-      return landed(c) && wait_warp(vt_bar(c), phase2(c)) &&
-             (!kOut || c == 0 || wait_warp(b_kv_free, c - 1));
-    };
-    bool go = n_chunks > 0 && kv_ready(0);
-    for (int c = 0; c < n_chunks && go; ++c) {
-      const int s = c % kStages;
-      const uint64_t st = static_cast<uint64_t>(s * STAGE) >> 4;
-      tc_fence_after();
-      const uint32_t kv = kv_col(c), vt = vt_col(c);
-      const uint64_t bk = dk_mn0 + st, aq = dq0 + st;
-      if (elected) {
-        // KV(c) = V'^T K, the smallest terms first
+        __syncwarp();
+        if (!kOut) {
+          go = c + 1 == n_chunks || kv_ready(c + 1);
+          continue;
+        }
+        if (c > 0 && !wait_warp(b_o_free, c - 1)) break;
+        tc_fence_after();
+        if (elected) {
+          // S(c) = Q K^T
+          const uint64_t bks = dk0 + st;
 #pragma unroll
-        for (int term = 2; term >= 0; --term)
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+            mma_bf16(tmem + TC_S, aq + off, bks + off, idesc_bf16(64, 64, false, false), kk > 0);
+          }
+          mma_commit(b_s);
+        }
+        __syncwarp();
+        if (!wait_warp(b_h, c)) break;
+        tc_fence_after();
+        if (elected) {
+          // OI(c) = H0^T Q^T
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ts(kv, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), idesc_bf16(128, 128, false, true),
-                        term < 2 || kk > 0);
-        mma_commit(kv_bar(c));
-      }
-      __syncwarp();
-      if (!kOut) {
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8, aq + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
+                          idesc_bf16(128, 64, false, false), part < 1 || kk > 0);
+        }
+        __syncwarp();
+        if (!wait_warp(b_p, c)) break;
+        tc_fence_after();
+        if (elected) {
+          // PV(c) = V^T P^T
+          const uint64_t av = dv_mn0 + st;
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), dp + ((part * HALF + kk * 32) >> 4),
+                       idesc_bf16(128, 64, true, false), part < 1 || kk > 0);
+          mma_commit(b_o);
+        }
+        __syncwarp();
         go = c + 1 == n_chunks || kv_ready(c + 1);
-        continue;
       }
-      if (c > 0 && !wait_warp(b_o_free, c - 1)) break;
-      tc_fence_after();
       if (elected) {
-        // S(c) = Q K^T
-        const uint64_t bks = dk0 + st;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-          mma_bf16(tmem + TC_S, aq + off, bks + off, idesc_bf16(64, 64, false, false), kk > 0);
-        }
-        mma_commit(b_s);
+        mma_commit(b_drain);   // every product issued is complete before tensor memory is released
+        mbar_wait(b_drain, 0, p.err, 1u << 20);
       }
       __syncwarp();
-      if (!wait_warp(b_h, c)) break;
-      tc_fence_after();
-      if (elected) {
-        // OI(c) = H0^T Q^T
-#pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + TC_OI, tmem + TC_H + part * 64 + kk * 8, aq + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
-                        idesc_bf16(128, 64, false, false), part < 1 || kk > 0);
-      }
-      __syncwarp();
-      if (!wait_warp(b_p, c)) break;
-      tc_fence_after();
-      if (elected) {
-        // PV(c) = V^T P^T
-        const uint64_t av = dv_mn0 + st;
-#pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tmem + TC_PV, av + ((kk * 2048) >> 4), dp + ((part * HALF + kk * 32) >> 4),
-                     idesc_bf16(128, 64, true, false), part < 1 || kk > 0);
-        mma_commit(b_o);
-      }
-      __syncwarp();
-      go = c + 1 == n_chunks || kv_ready(c + 1);
     }
-    if (elected) {
-      mma_commit(b_drain);   // every product issued is complete before tensor memory is released
-      mbar_wait(b_drain, 0, p.err, 1u << 20);
-    }
-    __syncwarp();
-   }
   } else if (warp < 4) {
     regs_dec<kRegsOut>();
     if (kOut) {
@@ -907,7 +918,8 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
     main.add(split * hv, len);
     for (int n = 0; n < n_seqs; ++n) main.add(hv, nc[n] > 0 ? (nc[n] - 1) % len + 1 : 0);
     const double base = main.time() + 4.0;
-    // a whole segment on each SM, or two thirds and a third (two thirds of the SMs, then all)
+    // an early segment whole, or as two thirds and a third, which two thirds of 148 SMs and the rest
+    // take side by side (32 768 tokens, 48 heads: 481 us whole, 461 us in pieces)
     for (int part : {len, (2 * len + 2) / 3}) {
       const int pieces = (len + part - 1) / part;
       Launch state;
@@ -953,7 +965,12 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
     e = cudaFuncSetAttribute(decay_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(decay_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return launch_status(e, "decay prefill: shared memory opt-in");
+    cudaFuncAttributes with{}, without{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&with, decay_prefill_kernel<true>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&without, decay_prefill_kernel<false>);
+    // built with fewer registers, the state's warps would wait for more than the block has
+    if (e == cudaSuccess && (with.numRegs < kRegsLaunch || without.numRegs < kRegsLaunch)) e = cudaErrorInvalidKernelImage;
+    if (e != cudaSuccess) return launch_status(e, "decay prefill: set-up");
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
   if (!tensor_map_encoder())

@@ -77,7 +77,8 @@ GDR_API const char *gdr_status_string(int status);
  * changes (2: the conv fused into gdr_chunk_prefill,
  * gdr_chunk_prefill_fused_workspace_size; 3: gdr_decode_step_slots; 4:
  * gdr_chunk_prefill_slots; 5: gdr_chunk_prefill_schedule and the
- * pipelined window schedule; 6: gdr_linear). */
+ * pipelined window schedule; 6: gdr_linear).  The calls of decayed linear
+ * attention and gdr_block_norm were added under 6: they change no other call. */
 GDR_API int gdr_abi_version(void);
 
 /*
@@ -423,7 +424,7 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  */
 
 /*
- * gdr_decay_attn_prefill -- the recurrence over packed sequences.
+ * gdr_decay_attn_prefill -- the recurrence over packed sequences (at most 65535).
  *   cu_seqlens_dev / cu_seqlens_host: [n_seqs + 1] int32, same values.  Rows of o
  *             behind the last sequence are left as they were.
  *   h0:       fp32 [n_seqs][hv][128][128] initial state, or NULL = zeros

@@ -226,6 +226,19 @@ def test_prefill_refusals(L):
     assert call(True, ch=cup([0, 0, 0])[1], ns=0, pool=None, q=None, k=None, v=None, o=None, cd=None) == 0
 
 
+def test_prefill_refuses_bad_workspaces(L):
+    """4096 tokens of four heads run in segments, whose states need a workspace."""
+    keep, c = cup([0, 4096])
+    need = L.gdr_decay_attn_prefill_workspace_size(c, 1, 4)
+    assert need > 0 and need % (4 * D * D * 4) == 0
+    assert L.gdr_decay_attn_prefill_workspace_size(cup([0, 200])[1], 1, 4) == 0
+    call = lambda ws, nbytes, hT=P + 3 * GB: L.gdr_decay_attn_prefill(   # noqa: E731
+        P, P + GB, P + 2 * GB, 0, 0, 0, P, 1.0, 2, 4, P, c, 1, None, hT, P + 4 * GB, ws, nbytes, None)
+    assert call(None, need) == 6 and call(P + 5 * GB, need - 1) == 6 and call(P + 5 * GB + 8, need) == 3
+    assert call(P + 4 * GB + 4096, need) == 9 and call(P + 2 * GB, need) == 9      # on o, on v
+    assert call(P + 3 * GB - need + 16, need) == 9                                  # its end on hT
+
+
 def test_decode_refusals(L):
     def call(slots=False, **kw):
         a = dict(q=P, k=P + GB, v=P + 2 * GB, qs=0, ks=0, vs=0, g=P, scale=1.0, hk=2, hv=4, st=P + 3 * GB, ns=4, slot=P,

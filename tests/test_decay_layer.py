@@ -13,7 +13,7 @@ import gated_delta_rule_63_b200 as G
 from oracle import oracle as O
 from tests.test_block_norm import check as check_norm
 from tests.test_decay_attn import E, U, check as check_attn
-from tests.helpers import bits_f64, host_bits, ulp_diff_bf16
+from tests.helpers import host_bits, ulp_diff_bf16
 
 pytestmark = pytest.mark.gpu
 D, HK, HV, HID = 128, 1, 3, 256
@@ -65,10 +65,8 @@ def check_step(L, x, residual, s, cu, h0, states):
                                     w_pre=L.w_pre.cpu().numpy(), alpha=1.0), False)
     check_attn(s["o"], states, f64(s["q"]), f64(s["k"]), f64(s["v"]), L.log_decay.cpu().numpy(), cu, h0, D ** -0.5)
     # gated norm: at most one bf16 step from the rounded oracle; projections: half a step and fp32 sums
-    ref = O.gated_rmsnorm(f64(s["o"]), f64(s["z"]), L.norm_w.cpu().numpy())
-    ref = ref[0] if isinstance(ref, tuple) else ref
-    ref_bits = ref if np.asarray(ref).dtype == np.uint16 else O.round_bf16(np.asarray(ref))
-    assert int(ulp_diff_bf16(host_bits(s["y"]), np.asarray(ref_bits).reshape(s["y"].shape)).max()) <= 1
+    ref = O.round_bf16(O.gated_rmsnorm(f64(s["o"]), f64(s["z"]), L.norm_w.cpu().numpy()))
+    assert int(ulp_diff_bf16(host_bits(s["y"]), ref).max()) <= 1
     for a, w, got in ((f64(s["h"]), f64(L.w_in), s["p"]), (f64(s["y"]).reshape(len(x), -1), f64(L.w_out), s["out"])):
         exact, size = a @ w.T, np.abs(a) @ np.abs(w).T
         assert np.all(np.abs(f64(got) - exact) <= U * np.abs(exact) * (1 + U) + a.shape[1] * E * size)
