@@ -916,6 +916,9 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
     int units = 0;
     for (int n = 0; n < n_seqs; ++n) units += std::max(1, (nc[n] + len - 1) / len);
     const int split = units - n_seqs;
+    const double extra = 4.0 + 0.6 * (s - 1);
+    if (std::max<double>(len, static_cast<double>(load) / kSms) + 0.42 * split * len * hv / kSms + extra >= least)
+      continue;   // not even with every SM busy to the end
     Launch main;
     main.add(split * hv, len);
     for (int n = 0; n < n_seqs; ++n) main.add(hv, nc[n] > 0 ? (nc[n] - 1) % len + 1 : 0);

@@ -380,6 +380,20 @@ size_t span_bytes(int64_t rows, int64_t stride, int64_t width, size_t size) {
   return rows <= 0 ? 0 : (static_cast<size_t>(rows - 1) * stride + width) * size;
 }
 
+// Rows of `width` bytes, `stride` bytes apart (null: none).
+struct Rows {
+  const void *at;
+  int64_t rows, stride, width;
+  bool meets(const Rows &b) const {
+    if (!overlaps(at, span_bytes(rows, stride, width, 1), b.at, span_bytes(b.rows, b.stride, b.width, 1))) return false;
+    if (stride != b.stride || stride == 0) return true;
+    // rows side by side in one buffer, like the slices of a packed projection, do not meet
+    int64_t off = (static_cast<const char *>(b.at) - static_cast<const char *>(at)) % stride;
+    if (off < 0) off += stride;
+    return off < width || off + b.width > stride;
+  }
+};
+
 // Token strides of q, k, v: 0 is dense; otherwise at least a row and a multiple of 8.
 int decay_strides(int hk, int hv, int64_t *qs, int64_t *ks, int64_t *vs) {
   const int64_t qk = static_cast<int64_t>(hk) * kHeadDim, vv = static_cast<int64_t>(hv) * kHeadDim;
@@ -550,19 +564,17 @@ int gdr_block_norm(const gdr_block_norm_t *a, int64_t rows, int64_t d, void *str
       !aligned16(a->residual_out) || !aligned16(a->w_pre) || !aligned16(a->y))
     return GDR_ERR_ALIGN;
   const size_t rs = a->residual_fp32 ? 4 : 2;
-  const size_t xb = span_bytes(rows, p.x_stride, d, 2), yb = span_bytes(rows, p.y_stride, d, 2);
-  const size_t gb = a->gate_shared ? static_cast<size_t>(d) * 2 : span_bytes(rows, p.gate_stride, d, 2);
-  const size_t ib = span_bytes(rows, p.res_stride, d, rs), ob = span_bytes(rows, p.out_stride, d, rs);
-  const size_t wb = static_cast<size_t>(d) * 4;
+  const Rows x{a->x, rows, p.x_stride * 2, d * 2}, y{a->y, rows, p.y_stride * 2, d * 2};
+  const Rows gate{a->gate, a->gate_shared ? 1 : rows, p.gate_stride * 2, d * 2};
+  const Rows in{a->residual, rows, p.res_stride * static_cast<int64_t>(rs), d * static_cast<int64_t>(rs)};
+  const Rows out{a->residual_out, rows, p.out_stride * static_cast<int64_t>(rs), d * static_cast<int64_t>(rs)};
+  const Rows w_post{a->w_post, 1, 0, d * 4}, w_pre{a->w_pre, 1, 0, d * 4};
   // in place where every value is read by the thread that writes it: residual_out on residual, y on x
   const bool res_in_place = a->residual == a->residual_out && p.res_stride == p.out_stride;
   const bool y_in_place = static_cast<const void *>(a->y) == a->x && p.y_stride == p.x_stride;
-  if (overlaps(a->y, yb, a->residual_out, ob) || overlaps(a->y, yb, a->residual, ib) ||
-      overlaps(a->y, yb, a->gate, gb) || overlaps(a->y, yb, a->w_post, wb) || overlaps(a->y, yb, a->w_pre, wb) ||
-      (!y_in_place && overlaps(a->y, yb, a->x, xb)) || overlaps(a->residual_out, ob, a->x, xb) ||
-      overlaps(a->residual_out, ob, a->gate, gb) || overlaps(a->residual_out, ob, a->w_post, wb) ||
-      overlaps(a->residual_out, ob, a->w_pre, wb) ||
-      (!res_in_place && overlaps(a->residual_out, ob, a->residual, ib)))
+  if (y.meets(out) || y.meets(in) || y.meets(gate) || y.meets(w_post) || y.meets(w_pre) ||
+      (!y_in_place && y.meets(x)) || out.meets(x) || out.meets(gate) || out.meets(w_post) || out.meets(w_pre) ||
+      (!res_in_place && out.meets(in)))
     return GDR_ERR_ALIAS;
   p.x = static_cast<const uint16_t *>(a->x);
   p.w_post = a->w_post;

@@ -498,7 +498,8 @@ GDR_API int gdr_decay_attn_decode_slots(const void *q, const void *k, const void
  * d is a multiple of 8, at most 32768 (GDR_ERR_UNSUPPORTED above).
  * Strides are between rows, in elements, 0 = dense (d), else at least d and a multiple
  * of 8.  In place: residual_out may equal residual and y may equal x, with equal
- * strides; the outputs overlap nothing else (GDR_ERR_ALIAS).
+ * strides; the outputs overlap nothing else (GDR_ERR_ALIAS; slices of one buffer with
+ * one stride, side by side, do not overlap).
  */
 typedef struct gdr_block_norm {
   const void *x;               /* bf16 [rows][d] output of the block */

@@ -83,6 +83,11 @@ def test_refusals():
     assert call(gate=P + 3 * GB + 4 * one - 16, gate_shared=1) == 9   # y's last values are the gate
     assert call(w_pre=P + 2 * GB) == 9
     assert call(rows=0, x=None) == 0
+    # rows side by side in one buffer meet only where their columns do
+    side = dict(x_stride=256, y_stride=256)
+    assert call(**side, x=P, y=P + one - 16) == 9 and call(**side, x=P + one, y=P + 16) == 9
+    assert call(**side, x=P, y=P + 512 * 3 + one - 16) == 9       # the same, some rows on
+    assert call(x=P, x_stride=256, y=P + one, y_stride=128) == 9  # with other strides they may
 
 
 def test_binding_refuses_cpu_tensors():
@@ -185,6 +190,20 @@ def test_in_place_and_strided_rows(gpu, wide):
     r3, y3 = G.block_norm(**{**t, "x": xs, "residual": rs, "gate": gs}, residual_out=rs, y=xs)
     assert torch.equal(rs, r) and torch.equal(xs, y)
     assert bool(torch.isnan(xb[:, d:]).all()) and bool(torch.isnan(rb[:, d:]).all())
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gpu):
+    """Rows 2^20 values apart: the last ones lie past 2^31 values.  The bits of the dense call."""
+    rows, d, wide = 2200, 640, 1 << 20
+    t = to_dev(make(7, rows, d, False, True, "row"), False)
+    buf = torch.empty(rows, wide, dtype=torch.bfloat16, device="cuda")
+    parts = [buf[:, i * d:(i + 1) * d] for i in range(5)]
+    for p, name in zip(parts, ("x", "residual", "gate")):
+        p.copy_(t[name])
+    r, y = G.block_norm(**t)
+    G.block_norm(**{**t, "x": parts[0], "residual": parts[1], "gate": parts[2]}, residual_out=parts[1], y=parts[0])
+    assert torch.equal(parts[1], r) and torch.equal(parts[0], y)
 
 
 @pytest.mark.gpu

@@ -539,6 +539,33 @@ def test_calls_on_streams_and_in_graphs(gpu):
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits(gpu):
+    """Rows 2^20 values apart and a pool of 140 000 entries: the last offsets are past 2^31 values.
+    The same calls on dense copies and a small pool give the same bits."""
+    T, wide, entries = 2200, 1 << 20, 140_000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rows = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")
+    for x in (rows[:, :D], rows[:, D:2 * D], rows[:, -D:]):
+        x.copy_(torch.randn(T, D, generator=gen, device="cuda"))
+    q, k, v = rows[:, None, :D], rows[:, None, D:2 * D], rows[:, None, -D:]
+    g = torch.tensor([-0.01], device="cuda")
+    pool = torch.empty(entries, 1, D, D, device="cuda")
+    small = torch.randn(2, 1, D, D, generator=gen, device="cuda")
+    pool[entries - 1] = small[1]
+    cu = np.array([0, T], np.int32)
+    cu_d = torch.tensor(cu, device="cuda")
+    far, near = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in (entries - 1, 1))
+    o = G.decay_attn_prefill_slots(q, k, v, g, cu_d, cu, pool, far, init_from_pool=True)
+    o2 = G.decay_attn_prefill_slots(*(x.contiguous() for x in (q, k, v)), g, cu_d, cu, small, near, init_from_pool=True)
+    assert torch.equal(o, o2) and torch.equal(pool[entries - 1], small[1])
+    # the last two rows as tokens of two sequences, the first of them a padding row
+    far, near = (torch.tensor([-1, i], dtype=torch.int32, device="cuda") for i in (entries - 1, 1))
+    o = G.decay_attn_decode_slots(q[-2:], k[-2:], v[-2:], g, pool, far)
+    o2 = G.decay_attn_decode_slots(*(x[-2:].contiguous() for x in (q, k, v)), g, small, near)
+    assert torch.equal(o, o2) and torch.equal(pool[entries - 1], small[1])
+
+
+@pytest.mark.gpu
 def test_binding_refuses_on_the_gpu(gpu):
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")   # noqa: E731
     cu = np.array([0, 4], np.int32)
