@@ -142,9 +142,15 @@ def _check(fn: str, code: int):
 # marshalling helpers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, dtype=None, name="tensor", rows=False):
@@ -460,31 +466,33 @@ def linear(x, w, y=None, stream=None):
 
 class _Call:
     """Device and stream of a call, taken from its first tensor; every other must be there too."""
-    __slots__ = ("torch", "index")
+    __slots__ = ("torch", "tensor", "index")
 
     def __init__(self, t, name):
         self.torch = torch = _torch()
+        self.tensor = torch.Tensor
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
+        self.index = t.get_device()   # -1 for the host
+        if self.index < 0 or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        self.index = t.get_device()
 
-    def check(self, t, dtype, name):
-        if not isinstance(t, self.torch.Tensor):
+    def refuse(self, t, dtype, name):
+        """What is wrong with a tensor's type, dtype or device."""
+        if not isinstance(t, self.tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != self.index:   # -1 for the host
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            raise ValueError(f"tensors on cuda:{self.index} and {t.device}: all tensors of a call must be on one device")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"tensors on cuda:{self.index} and {t.device}: all tensors of a call must be on one device")
 
     def dense(self, t, dtype, name, shape):
         """Pointer of a contiguous tensor of that shape (None passes)."""
         if t is None:
             return None
-        self.check(t, dtype, name)
+        if not isinstance(t, self.tensor) or t.dtype is not dtype or t.get_device() != self.index:
+            self.refuse(t, dtype, name)
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
@@ -493,9 +501,12 @@ class _Call:
 
     def heads(self, t, name, rows, heads):
         """(pointer, token stride) of a bf16 [>= rows, heads, 128] tensor whose last two dims are dense."""
-        self.check(t, self.torch.bfloat16, name)
-        if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.shape[1] != heads or t.shape[0] < rows:
-            raise ValueError(f"{name} must be [{rows}, {heads}, {HEAD_DIM}], got {tuple(t.shape)}")
+        bf16 = self.torch.bfloat16
+        if not isinstance(t, self.tensor) or t.dtype is not bf16 or t.get_device() != self.index:
+            self.refuse(t, bf16, name)
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != HEAD_DIM or shape[1] != heads or shape[0] < rows:
+            raise ValueError(f"{name} must be [{rows}, {heads}, {HEAD_DIM}], got {tuple(shape)}")
         if t.is_contiguous():
             return t.data_ptr(), 0
         st = t.stride()
@@ -507,7 +518,8 @@ class _Call:
         """(pointer, row stride) of `rows` rows of d values: contiguous, or [rows, d] with dense rows."""
         if t is None:
             return None, 0
-        self.check(t, dtype, name)
+        if not isinstance(t, self.tensor) or t.dtype is not dtype or t.get_device() != self.index:
+            self.refuse(t, dtype, name)
         if t.numel() != rows * d or t.shape[-1] != d:
             raise ValueError(f"{name} must hold {rows} rows of {d} values, got {tuple(t.shape)}")
         if t.is_contiguous():
@@ -518,20 +530,28 @@ class _Call:
 
     def run(self, name, fn, stream, *args):
         """fn(*args, stream) on the call's device."""
-        torch = self.torch
+        cuda, index = self.torch.cuda, self.index
         if stream is None:
-            handle = torch.cuda.current_stream(self.index).cuda_stream
+            handle = _current_stream(index)
         else:
-            if getattr(stream, "device", None) is not None and stream.device.index != self.index:
-                raise ValueError(f"stream on {stream.device}, tensors on cuda:{self.index}")
+            if getattr(stream, "device", None) is not None and stream.device.index != index:
+                raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
             handle = stream.cuda_stream
-        if torch.cuda.current_device() == self.index:
+        if cuda.current_device() == index:
             code = fn(*args, handle)
         else:
-            with torch.cuda.device(self.index):
+            with cuda.device(index):
                 code = fn(*args, handle)
         if code != 0:
             raise GdrError(name, code)
+
+
+def _current_stream(index):
+    """Handle of the current stream of a device: torch's own short way where it has one (making the
+    Stream object takes 1.2 us, a tenth of a short call)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _on_stream(stream, make):
@@ -560,7 +580,8 @@ def _decay_o(call, o, v, hv, rows, stream):
     """o (made when None) and its pointer; it may have more rows than the call writes."""
     torch = _torch()
     if o is None:
-        o = _on_stream(stream, lambda: torch.empty_like(v))   # v's shape, dense (v has dense rows)
+        # v's shape, dense (v has dense rows)
+        o = torch.empty_like(v) if stream is None else _on_stream(stream, lambda: torch.empty_like(v))
         return o, o.data_ptr()
     if isinstance(o, torch.Tensor) and (o.dim() != 3 or o.shape[0] < rows):
         raise ValueError(f"o must be [{rows}, {hv}, {HEAD_DIM}], got {tuple(o.shape)}")
@@ -665,21 +686,26 @@ def block_norm(x, residual=None, gate=None, post_norm: bool = False, w_post=None
     torch = _torch()
     bf, f32 = torch.bfloat16, torch.float32
     call = _Call(x, "x")
-    d = int(x.shape[-1]) if x.dim() else 0
+    d = x.shape[-1] if x.dim() else 0
     rows = x.numel() // d if d else 0
+    xp, xs = call.rows(x, bf, "x", rows, d)
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else bf
     if rdt is not bf and rdt is not f32:
         raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {rdt}")
-    if residual_out is None and want_residual:
-        residual_out = _on_stream(stream, lambda: torch.empty_like(x, dtype=rdt))
-    if y is None and want_y:
-        y = _on_stream(stream, lambda: torch.empty_like(x))
     shared = gate is not None and gate.dim() == 1
-    xp, xs = call.rows(x, bf, "x", rows, d)
     gp, gs = call.rows(gate, bf, "gate", 1 if shared else rows, d)
     rp, rs = call.rows(residual, rdt, "residual", rows, d)
-    op, os_ = call.rows(residual_out, rdt, "residual_out", rows, d)
-    yp, ys = call.rows(y, bf, "y", rows, d)
+    if residual_out is None and want_residual:   # (x's shape, dense)
+        make = (lambda: torch.empty_like(x)) if rdt is bf else (lambda: torch.empty_like(x, dtype=rdt))
+        residual_out = make() if stream is None else _on_stream(stream, make)
+        op, os_ = residual_out.data_ptr(), 0
+    else:
+        op, os_ = call.rows(residual_out, rdt, "residual_out", rows, d)
+    if y is None and want_y:
+        y = torch.empty_like(x) if stream is None else _on_stream(stream, lambda: torch.empty_like(x))
+        yp, ys = y.data_ptr(), 0
+    else:
+        yp, ys = call.rows(y, bf, "y", rows, d)
     args = BlockNormArgs(xp, xs, 1 if post_norm else 0, call.dense(w_post, f32, "w_post", (d,)),
                          eps if eps_post is None else eps_post, gp, gs, 1 if shared else 0, alpha, rp, rs,
                          1 if rdt == f32 else 0, op, os_, call.dense(w_pre, f32, "w_pre", (d,)), eps, yp, ys)
