@@ -81,7 +81,7 @@ constexpr int kThreads = 512;
 // Registers a thread.  512 threads have 128 each at launch, the whole file; warps 12..15 and 0..3 give
 // some of theirs to the state's warps, which spilled 740 bytes without (107 instead of 81 us for a
 // prompt of 4096 tokens).  The launcher checks that the launch has them to give.
-constexpr int kRegsLaunch = 128, kRegsFew = 56, kRegsOut = 120, kRegsState = 168;
+constexpr int kRegsLaunch = 128, kRegsFew = 48, kRegsOut = 112, kRegsState = 176;
 static_assert(128 * kRegsFew + 128 * kRegsOut + 256 * kRegsState <= kThreads * kRegsLaunch, "register split");
 constexpr int kStages = 4;
 constexpr int kSms = 148;
