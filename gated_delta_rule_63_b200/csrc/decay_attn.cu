@@ -41,9 +41,9 @@
 //   full[s]      the copies of a chunk landed -> the products may read them, V' may be made
 //   empty[s]     the chunk's last product is done -> its stage may be refilled (arrived at by a warp
 //                that waits for that product: a commit holds the issuing lane for some 130 cycles)
-//   vt[]         V' of chunk c is in TMEM, a partial chunk's tail rows are zero -> KV(c), S(c)
+//   vt[]         V' of chunk c is in TMEM, the state has read KV(c - 1) (KV(c - 2) without output), a
+//                partial chunk's tail rows are zero -> KV(c), S(c)
 //   kv[]         KV(c) is done -> the state takes it, V' may be rewritten
-//   kv_free      the state has read KV(c) -> KV(c + 1) may overwrite it
 //   s            S(c) is done -> P(c)
 //   h            H before chunk c is in TMEM -> OI(c)
 //   p            P(c) is in shared memory -> PV(c)
@@ -349,7 +349,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint8_t *smem = smem_raw + (sbase - raw_addr);
   volatile uint8_t *bad = smem + OFF_BAD;
   const uint32_t b_full = sbase + OFF_BAR, b_empty = b_full + 8 * kStages, b_vt = b_empty + 8 * kStages;
-  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_kv_free = b_kv + 24, b_h = b_kv + 32,
+  const uint32_t b_kv = b_vt + 16, b_s = b_kv + 16, b_h = b_kv + 32,
                  b_p = b_kv + 48, b_o = b_kv + 56, b_o_free = b_kv + 64, b_drain = b_kv + 72;
   constexpr uint32_t kWords = 8 * (2 * kStages + 2 + 10);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + OFF_BAR + kWords);
@@ -366,7 +366,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(b_kv, 1);
     mbar_init(b_kv + 8, 1);
     mbar_init(b_s, 1);
-    mbar_init(b_kv_free, 8);
     mbar_init(b_h, 8);
     mbar_init(b_p, 4);
     mbar_init(b_o, 1);
@@ -465,8 +464,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
       const uint64_t dp = sdesc(sbase + OFF_P, 16, 1024);
       const auto kv_ready = [&](int c) {   // KV(c) may be issued
-        return landed(c) && wait_warp(vt_bar(c), phase2(c)) &&
-               (!kOut || c == 0 || wait_warp(b_kv_free, c - 1));
+        return landed(c) && wait_warp(vt_bar(c), phase2(c));
       };
       bool go = n_chunks > 0 && kv_ready(0);
       for (int c = 0; c < n_chunks && go; ++c) {
@@ -742,11 +740,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         float kv[32];
         tmem_ld32(kv_col(c) + quarter + 64 * half + 32 * part, kv);
         tmem_wait_ld();
-        if (kOut && part == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_kv_free);
-        }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           H[16 * part + e] = now.apply2(H[16 * part + e], make_float2(kv[2 * e], kv[2 * e + 1]));
@@ -820,15 +813,15 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (go) finish_h();   // (KV(0) and S(0) need no state)
       if (n_chunks > 0 && go) put_h();
       for (int c = 0; c < n_chunks && go; ++c) {
-        // while the products of chunk c run: V'(c + 1) first, which KV(c + 1) waits for
+        // while the products of chunk c run
         const bool more = c + 1 < n_chunks;
         if (more) {
           if (!(go = landed(c + 1))) break;
           begin_vt(c + 1);
         }
         if (!(go = kv_done(c))) break;
-        if (more) finish_vt(c + 1);
         take_kv(c);
+        if (more) finish_vt(c + 1);
         if (more) {
           if (!(go = wait_warp(b_o, c))) break;   // (OI(c) is done with the H before)
           tc_fence_after();
