@@ -11,22 +11,23 @@
 //
 // The products, transposed so that M = 128 rows are used wherever they can be:
 //     S   = Q K^T                 M = 64 (tokens),  N = 64,  K = 128
-//     KV  = V'^T K                M = 128 (dv),     N = 128, K = 64;  V' in three bf16 terms
+//     KV  = V'^T K                M = 128 (dv),     N = 128, K = 64;  V' in three or two bf16 terms
 //     OI  = H0^T Q^T              M = 128 (dv),     N = 64,  K = 128; H0 in two bf16 terms
 //     PV  = V^T P^T               M = 128 (dv),     N = 64,  K = 64;  P in two bf16 terms
 // q, k, v are bf16 and exact.  H0 and P (fp32) as hi + lo bf16 keep 16 bits of them, an error
-// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the state stays an
-// fp32 sum (two terms would leave it an error of about 2.7e-6, ten times that of fp32 sums).
+// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the final state is an
+// fp32 sum (two terms would leave it an error of about 2.7e-6, ten times that of fp32 sums), but
+// for chunks of which the final state keeps too little for the third term to show in it.
 //
 // V' and H0 are A operands in tensor memory, written from registers: as shared-memory tiles they
 // took the bandwidth that the products read their operands with (149 -> 92 us for a prompt of 4096
 // tokens and 48 value heads, with o and V going through 8 x 8 transposes).
 //
-// What bounds it: the products of a chunk, 13.6 MFLOP (44 MMAs), keep the tensor pipe for about
-// 2900 of a chunk's 3150 cycles (an M = 128, N = 64, K = 16 product with A in tensor memory
-// takes 70 cycles, N = 128 79).  32 768 tokens of 48 value heads take 461 us: 0.9 PFLOP/s of such
-// products with those of the segments' states, 1.08 GB read and written once at 2.3 TB/s; a
-// prompt of 4096 tokens 69 us.  The GPU then runs at its power cap, at about 1.6 GHz.
+// What bounds it: the products of a chunk, 11.5 or 13.6 MFLOP (40 or 44 MMAs), keep the tensor pipe
+// for 2600 or 2900 of a chunk's 3090 cycles (an M = 128, N = 64, K = 16 product with A in tensor
+// memory takes 70 cycles, N = 128 79), and S -> P -> PV -> o -> the next S, which share columns, is
+// a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 65 us; 32 768
+// tokens take 413 us, 1.08 GB read and written once at 2.6 TB/s, with the GPU at its power cap.
 //
 // One CTA (16 warps, the last two idle) walks the chunks of one (value head, sequence or segment):
 //   warps 0..3   P from S (TMEM -> registers -> shared memory), and o from OI and PV
@@ -58,8 +59,8 @@
 // run beside each other: a first launch (kOut = false: K and V only) leaves what each segment
 // but the last adds to the state, a second one starts every segment from the decayed sum of
 // those before it.  plan_decay() weighs the extra pass against the shorter chain; measured, in
-// one piece and as it chooses: 512 tokens of 48 value heads 19.7 (not cut), 1024 33.2 and 27.4,
-// 4096 114 and 68.5, 16 384 437 and 228 us; 4096 of 16 heads 113 and 42.6, 8192 of 2 219 and 41 us.
+// one piece and as it chooses: 512 tokens of 48 value heads 19.4 (not cut), 1024 32.6 and 26.4,
+// 4096 112 and 65, 16 384 413 and 212 us; 4096 of 16 heads 111 and 41, 8192 of 2 213 and 38.6 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -80,7 +81,8 @@ constexpr int C = kChunk;            // tokens of a chunk
 constexpr int kThreads = 512;
 // Registers a thread.  512 threads have 128 each at launch, the whole file; warps 12..15 and 0..3 give
 // some of theirs to the state's warps, which spilled 740 bytes without (107 instead of 81 us for a
-// prompt of 4096 tokens).  The launcher checks that the launch has them to give.
+// prompt of 4096 tokens); 56 / 120 / 168 took 69.5 us where these take 68.4.  The launcher checks that
+// the launch has them to give.
 constexpr int kRegsLaunch = 128, kRegsFew = 48, kRegsOut = 112, kRegsState = 176;
 static_assert(128 * kRegsFew + 128 * kRegsOut + 256 * kRegsState <= kThreads * kRegsLaunch, "register split");
 constexpr int kStages = 4;
@@ -454,8 +456,8 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const bool elected = elect_one();
       // V's third term is there for the final state alone: o's products round H to 16 bits anyway.  So
       // KV goes without it in a segment whose state goes nowhere, and where what a chunk adds will have
-      // decayed to 2^-24, an fp32 step, of what comes behind it by the end of the sequence (32 768 tokens of
-      // 48 heads in 431 instead of 459 us: these products are a third of KV's).
+      // decayed to 2^-24, an fp32 step, by the end of the sequence (32 768 tokens of 48 heads in 433 instead
+      // of 461 us: these products are a third of KV's).
       const float g = p.log_decay[h];
       const int reach = g < 0.0f ? static_cast<int>(fminf(16.64f / -g, 1e9f)) : INT_MAX;
       const bool state_goes_on = !kOut || un.seg == un.segs - 1;
@@ -701,7 +703,7 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     };
     // The state before the first chunk, or the first piece of what lies before this segment: loads
     // alone, in flight while V'(0) is made.  (By a bulk copy through shared memory instead, and the
-    // final state back the same way: 76.4 instead of 71.1 us for a prompt of 4096 tokens.)
+    // final state back the same way: 76.4 instead of 71.3 us for a prompt of 4096 tokens.)
     const int64_t at = static_cast<int64_t>(64 * half) * D + dv;
     const float *src = nullptr;   // (a piece of the state-only launch that is not its sequence's first: zero)
     if (un.seg == 0 && un.piece == 0) {

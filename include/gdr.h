@@ -417,9 +417,9 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  *   o:         bf16 [T][hv][128], dense; must not overlap an input or a state
  *              (GDR_ERR_ALIAS)
  * Precision: sums and states in fp32.  In the chunked form of the prefill the
- * probabilities (q.k) l^(i-j) and the state that a chunk's queries read are rounded to
- * bf16 for the tensor cores (as o itself is); the state that is carried and returned is
- * not.  A value that is not finite makes its sequence's later outputs and its state not
+ * probabilities (q.k) l^(i-j) and the state that a chunk's queries read go to the tensor
+ * cores as two bf16 terms (16 bits of them; o itself has 8); the state that is returned
+ * has the error of fp32 sums.  A value that is not finite makes its sequence's later outputs and its state not
  * finite; earlier tokens' outputs and other sequences keep theirs.
  */
 
