@@ -402,7 +402,10 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   const auto wait = [&](uint32_t bar, int phase) { return chain_wait(bar, phase & 1, abort_flag, p.err); };
   // the same for all lanes of a warp: they go on, or give up, together
-  const auto wait_warp = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+  const auto wait_warp = [&](uint32_t bar, int phase) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+    return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
+  };
   // V' and KV of chunk c: their columns, barriers and the barriers' phase
   const auto vt_col = [&](int c) { return tmem + (kOut ? TC_VT : TC_VT2 + (c & 1) * VT_BUF); };
   const auto kv_col = [&](int c) { return tmem + (kOut || (c & 1) == 0 ? TC_KV : TC_KV2); };
