@@ -26,8 +26,8 @@
 // What bounds it: the products of a chunk, 11.5 or 13.6 MFLOP (40 or 44 MMAs), keep the tensor pipe
 // for 2600 or 2900 of a chunk's 3090 cycles (an M = 128, N = 64, K = 16 product with A in tensor
 // memory takes 70 cycles, N = 128 79), and S -> P -> PV -> o -> the next S, which share columns, is
-// a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 65 us; 32 768
-// tokens take 413 us, 1.08 GB read and written once at 2.6 TB/s, with the GPU at its power cap.
+// a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 65 to 67 us; 32 768
+// tokens take 413 to 430 us, 1.08 GB read and written once at 2.5 to 2.6 TB/s, at the power cap.
 //
 // One CTA (16 warps, the last two idle) walks the chunks of one (value head, sequence or segment):
 //   warps 0..3   P from S (TMEM -> registers -> shared memory), and o from OI and PV
