@@ -1040,11 +1040,13 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
   p.o = static_cast<uint16_t *>(o);
   p.err = device_error_ptr();
   if (plan.seg_chunks != 0) {
-    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, dim3(hv, plan.early * plan.pieces), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
+    const int st = launch_status(launch_pdl(decay_prefill_kernel<false>, dim3(hv, plan.early * plan.pieces), dim3(kThreads), kSmem,
+                                            s, 1, tq, tk, tv, to, p),
                                  "decay prefill: segment kernel launch");
     if (st) return st;
   }
-  return launch_status(launch_pdl(decay_prefill_kernel<true>, dim3(hv, plan.units), dim3(kThreads), kSmem, s, 1, tq, tk, tv, to, p),
+  return launch_status(launch_pdl(decay_prefill_kernel<true>, dim3(hv, plan.units), dim3(kThreads), kSmem,
+                                  s, 1, tq, tk, tv, to, p),
                        "decay prefill: kernel launch");
 }
 
