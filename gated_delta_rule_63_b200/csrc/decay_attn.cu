@@ -15,9 +15,11 @@
 //     OI  = H0^T Q^T              M = 128 (dv),     N = 64,  K = 128; H0 in two bf16 terms
 //     PV  = V^T P^T               M = 128 (dv),     N = 64,  K = 64;  P in two bf16 terms
 // q, k, v are bf16 and exact.  H0 and P (fp32) as hi + lo bf16 keep 16 bits of them, an error
-// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the final state is an
-// fp32 sum (two terms would leave it an error of about 2.7e-6, ten times that of fp32 sums), but
-// for chunks of which the final state keeps too little for the third term to show in it.
+// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo) wherever it goes into the
+// final state, which is an fp32 sum then: its error is 0.7e-7 to 1.0e-7, where two terms, the second one
+// cut off, leave each value up to 2^-15 too small.  How far a chunk lies back says nothing about
+// what it is to the final state: the tokens after it may add nothing (a masked tail).  Segments whose
+// state is read by o alone go without the third term.
 //
 // V' and H0 are A operands in tensor memory, written from registers: as shared-memory tiles they
 // took the bandwidth that the products read their operands with (149 -> 92 us for a prompt of 4096
@@ -63,7 +65,6 @@
 // 4096 112 and 65, 16 384 413 and 212 us; 4096 of 16 heads 111 and 41, 8192 of 2 213 and 38.6 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <limits.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -313,12 +314,11 @@ struct Unit {
   int seq, seg, segs, piece;
   int slot;           // of the sequence's initial state; segment s's pieces are from 1 + s * pieces on
   int t_begin, t_end;
-  int seq_end;
 };
 template <bool kOut>
 __device__ __forceinline__ Unit find_unit(const DecayPrefillParams &p, int unit) {
-  if (p.n_seqs > kListed) return Unit{unit, 0, 1, 0, 0, p.cu[unit], p.cu[unit + 1], p.cu[unit + 1]};
-  if (p.seg_chunks == 0) return Unit{p.seq[unit], 0, 1, 0, 0, p.begin[unit], p.end[unit], p.end[unit]};
+  if (p.n_seqs > kListed) return Unit{unit, 0, 1, 0, 0, p.cu[unit], p.cu[unit + 1]};
+  if (p.seg_chunks == 0) return Unit{p.seq[unit], 0, 1, 0, 0, p.begin[unit], p.end[unit]};
   Unit u;
   u.piece = kOut ? 0 : unit / p.early;
   if (!kOut) unit -= u.piece * p.early;
@@ -331,7 +331,6 @@ __device__ __forceinline__ Unit find_unit(const DecayPrefillParams &p, int unit)
   u.segs = max(1, (chunks + p.seg_chunks - 1) / p.seg_chunks);
   u.t_begin = p.begin[i] + u.seg * p.seg_chunks * C;
   u.t_end = u.seg == u.segs - 1 ? p.end[i] : u.t_begin + p.seg_chunks * C;
-  u.seq_end = p.end[i];
   if (!kOut) {
     u.t_begin += u.piece * p.piece_chunks * C;
     u.t_end = min(u.t_end, u.t_begin + p.piece_chunks * C);
@@ -457,13 +456,10 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     } else if (warp == 13) {
       // ---- products
       const bool elected = elect_one();
-      // V's third term is there for the final state alone: o's products round H to 16 bits anyway.  So
-      // KV goes without it in a segment whose state goes nowhere, and where what a chunk adds will have
-      // decayed to 2^-24, an fp32 step, by the end of the sequence (32 768 tokens of 48 heads in 433 instead
-      // of 461 us: these products are a third of KV's).
-      const float g = p.log_decay[h];
-      const int reach = g < 0.0f ? static_cast<int>(fminf(16.64f / -g, 1e9f)) : INT_MAX;
-      const bool state_goes_on = !kOut || un.seg == un.segs - 1;
+      // V's third term is there for the final state: o's products round H to 16 bits anyway, and KV goes
+      // without it in a segment whose state goes nowhere (32 768 tokens of 48 heads in 443 instead of
+      // 452 us: these products are a third of KV's).
+      const bool three = !kOut || un.seg == un.segs - 1;
       // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
       const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
       const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
@@ -478,7 +474,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tc_fence_after();
         const uint32_t kv = kv_col(c), vt = vt_col(c);
         const uint64_t bk = dk_mn0 + st, aq = dq0 + st;
-        const bool three = state_goes_on && un.seq_end - min(t_begin + (c + 1) * C, t_end) <= reach;
         if (elected) {
           // KV(c) = V'^T K, the smallest terms first
           const auto issue_kv = [&](int term, bool add) {

@@ -1,0 +1,62 @@
+"""Decayed linear attention on a B200: the returned state has the error of fp32 sums, whatever the
+tokens after a chunk are (e = 2^-23, an fp32 step).
+
+One key per state row (keys e_0, e_1, ...): a chunk's product for a row is one value l^n v, held in
+three bf16 terms, and nothing cancels.  Its error, relative to the value: the argument g n is
+rounded once (|g n| e / 2 in the exponential), the exponential is good to 2 e, the product with v to
+e / 2, the sum of its three terms to a step each: at most 6 e + |g n| e / 2.  Every later chunk or
+piece multiplies by another exponential (2 e, and |g| 64 e / 2 from its argument) and adds (e / 2):
+3 e.  Over a sequence of L tokens in c chunks: (6 + |g| L / 2 + 3 c) e of the magnitudes' sum.
+Underflow adds what no relative bound covers: below 2^-126 an fp32 step is 2^-149, so each of those
+6 + 3 c roundings is off by at most 2^-149, times |v| < 8 where it is the factor that is rounded;
+and bf16's smallest step is 2^-133, below which a value's terms keep nothing: 2^-133 for each of the
+tokens that write to a row.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_63_b200 as G
+from oracle import oracle as O
+from tests.test_decay_attn import CH, D, E, check, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    G.lib()
+    yield
+    assert G.get_device_error() == 0
+
+
+@pytest.mark.parametrize("tail,decay", [(64, -0.5), (70, -0.3), (64, -1.0), (300, -0.06), (1700, -0.01)])
+def test_state_of_a_sequence_that_ends_in_zero_keys(tail, decay):
+    """64 ordinary tokens, then tokens that write nothing (a masked tail): the decayed sum of the
+    first ones is all there is.  The longest one runs in segments."""
+    q, k, v, cu, _ = make(51, [64 + tail], 1, 2)
+    k[64:] = 0.0
+    g = np.full(2, decay, np.float32)
+    o, hT = run(q, k, v, g, cu)
+    check(o, hT, q, k, v, g, cu, None, 1.0)
+
+
+@pytest.mark.parametrize("tokens,tail,decay", [(128, 42, -0.5), (128, 102, -0.3), (40, 64, -1.0), (128, 300, -0.06),
+                                               (128, 1722, -0.01), (128, 2300, -0.004), (700, 0, -0.004)])
+def test_state_of_one_key_a_row(tokens, tail, decay):
+    q, k, v, cu, _ = make(52, [tokens + tail], 1, 2)
+    k[:] = 0.0
+    at = np.arange(tokens)
+    k[at, 0, at % D] = 1.0
+    g = np.array([decay, 1.5 * decay], np.float32)
+    _, hT = run(q, k, v, g, cu)
+    _, ref = O.decay_attn(q, k, v, g, cu)
+    _, size = O.decay_attn(q, k, np.abs(v), g, cu)
+    L = int(cu[-1])
+    bound = (6 + np.abs(g.astype(np.float64)) * L / 2 + 3 * ((L + CH - 1) // CH)) * E
+    least = (6 + 3 * ((L + CH - 1) // CH)) * 8 * 2.0 ** -149 + (tokens // D + 1) * 2.0 ** -133
+    assert np.abs(v).max() < 8
+    err = np.abs(hT.double().cpu().numpy() - ref)[0]
+    assert np.all(err <= bound[:, None, None] * size[0] + least), float(np.max((err - least) / (E * size[0])))
