@@ -11,22 +11,22 @@
 //
 // The products, transposed so that M = 128 rows are used wherever they can be:
 //     S   = Q K^T                 M = 64 (tokens),  N = 64,  K = 128
-//     KV  = V'^T K                M = 128 (dv),     N = 128, K = 64;  V' in three or two bf16 terms
+//     KV  = V'^T K                M = 128 (dv),     N = 128, K = 64;  V' in three bf16 terms
 //     OI  = H0^T Q^T              M = 128 (dv),     N = 64,  K = 128; H0 in two bf16 terms
 //     PV  = V^T P^T               M = 128 (dv),     N = 64,  K = 64;  P in two bf16 terms
 // q, k, v are bf16 and exact.  H0 and P (fp32) as hi + lo bf16 keep 16 bits of them, an error
-// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo) wherever it goes into the
-// final state, which is an fp32 sum then: its error is 0.7e-7 to 1.0e-7, where two terms, the second one
-// cut off, leave each value up to 2^-15 too small.  How far a chunk lies back says nothing about
-// what it is to the final state: the tokens after it may add nothing (a masked tail).  Segments whose
-// state is read by o alone go without the third term.
+// far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the state is an fp32 sum in
+// every chunk: the final one's error is 0.7e-7 to 1.0e-7.  Two terms, the second one cut off, leave
+// each value up to 2^-15 too small.  Without the third one in chunks far back, the final state was wrong
+// wherever the tokens after them add nothing (a masked tail); without it in segments whose state is
+// read by o alone, o came out 5e-6 to 6e-6 too small (32 768 tokens of 48 heads in 443 instead of 452 us).
 //
 // V' and H0 are A operands in tensor memory, written from registers: as shared-memory tiles they
 // took the bandwidth that the products read their operands with (149 -> 92 us for a prompt of 4096
 // tokens and 48 value heads, with o and V going through 8 x 8 transposes).
 //
-// What bounds it: the products of a chunk, 11.5 or 13.6 MFLOP (40 or 44 MMAs), keep the tensor pipe
-// for 2600 or 2900 of a chunk's 3090 cycles (an M = 128, N = 64, K = 16 product with A in tensor
+// What bounds it: the products of a chunk, 13.6 MFLOP (44 MMAs), keep the tensor pipe
+// for 2900 of a chunk's 3090 cycles (an M = 128, N = 64, K = 16 product with A in tensor
 // memory takes 70 cycles, N = 128 79), and S -> P -> PV -> o -> the next S, which share columns, is
 // a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 65 to 67 us; 32 768
 // tokens take 413 to 430 us, 1.08 GB read and written once at 2.5 to 2.6 TB/s, at the power cap.
@@ -456,10 +456,6 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     } else if (warp == 13) {
       // ---- products
       const bool elected = elect_one();
-      // V's third term is there for the final state: o's products round H to 16 bits anyway, and KV goes
-      // without it in a segment whose state goes nowhere (32 768 tokens of 48 heads in 443 instead of
-      // 452 us: these products are a third of KV's).
-      const bool three = !kOut || un.seg == un.segs - 1;
       // descriptors are the base's plus a number of 16-byte units (addresses stay below 2^18)
       const uint64_t dk_mn0 = sdesc(sbase + OFF_K, HALF, 1024), dv_mn0 = sdesc(sbase + OFF_V, HALF, 1024);
       const uint64_t dq0 = sdesc(sbase + OFF_Q, 16, 1024), dk0 = sdesc(sbase + OFF_K, 16, 1024);
@@ -482,12 +478,8 @@ decay_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               mma_bf16_ts(kv, vt + term * VT_TERM + kk * 8, bk + ((kk * 2048) >> 4), idesc_bf16(128, 128, false, true),
                           add || kk > 0);
           };
-          if (three) {
-            issue_kv(2, false);
-            issue_kv(1, true);
-          } else {
-            issue_kv(1, false);
-          }
+          issue_kv(2, false);
+          issue_kv(1, true);
           issue_kv(0, true);
           mma_commit(kv_bar(c));
         }
