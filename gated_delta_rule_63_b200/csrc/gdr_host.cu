@@ -413,6 +413,14 @@ bool meets_inputs(const void *out, size_t bytes, const void *q, const void *k, c
          overlaps(out, bytes, v, span_bytes(rows, vs, static_cast<int64_t>(hv) * kHeadDim, 2));
 }
 
+// ... or one of the arrays the kernels read beside them (those that are null overlap nothing)
+bool meets_tables(const void *out, size_t bytes, const float *log_decay, int hv, const int32_t *slot, int n,
+                  const int32_t *cu) {
+  return overlaps(out, bytes, log_decay, static_cast<size_t>(hv) * 4) ||
+         overlaps(out, bytes, slot, static_cast<size_t>(n) * 4) ||
+         overlaps(out, bytes, cu, (static_cast<size_t>(n) + 1) * 4);
+}
+
 int decay_prefill(const void *q, const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
                   const float *log_decay, float scale, int hk, int hv, const int32_t *cu_dev,
                   const int32_t *cu_host, int n_seqs, const DecayStates &st, void *o, void *workspace,
@@ -434,6 +442,9 @@ int decay_prefill(const void *q, const void *k, const void *v, int64_t qs, int64
   if (meets_inputs(o, o_bytes, q, k, v, total, qs, ks, vs, hk, hv) ||
       meets_inputs(st_out, st_bytes, q, k, v, total, qs, ks, vs, hk, hv) ||
       meets_inputs(workspace, need, q, k, v, total, qs, ks, vs, hk, hv) ||
+      meets_tables(o, o_bytes, log_decay, hv, st.slot, n_seqs, cu_dev) ||
+      meets_tables(st_out, st_bytes, log_decay, hv, st.slot, n_seqs, cu_dev) ||
+      meets_tables(workspace, need, log_decay, hv, st.slot, n_seqs, cu_dev) ||
       overlaps(o, o_bytes, st_out, st_bytes) || overlaps(o, o_bytes, st.h0, st_bytes) ||
       overlaps(workspace, need, o, o_bytes) || overlaps(workspace, need, st_out, st_bytes) ||
       overlaps(workspace, need, st.h0, st_bytes) || (st.h0 != st.hT && overlaps(st.h0, st_bytes, st.hT, st_bytes)))
@@ -454,7 +465,9 @@ int decay_decode(const void *q, const void *k, const void *v, int64_t qs, int64_
   const size_t o_bytes = static_cast<size_t>(batch) * hv * kHeadDim * 2;
   const size_t st_bytes = static_cast<size_t>(entries) * hv * kStateElems * 4;
   if (meets_inputs(o, o_bytes, q, k, v, batch, qs, ks, vs, hk, hv) ||
-      meets_inputs(state, st_bytes, q, k, v, batch, qs, ks, vs, hk, hv) || overlaps(o, o_bytes, state, st_bytes))
+      meets_inputs(state, st_bytes, q, k, v, batch, qs, ks, vs, hk, hv) || overlaps(o, o_bytes, state, st_bytes) ||
+      meets_tables(o, o_bytes, log_decay, hv, slot, batch, nullptr) ||
+      meets_tables(state, st_bytes, log_decay, hv, slot, batch, nullptr))
     return GDR_ERR_ALIAS;
   return launch_decay_decode(q, k, v, qs, ks, vs, log_decay, scale, hk, hv, state, slot, entries, o, batch,
                              static_cast<cudaStream_t>(stream));

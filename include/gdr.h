@@ -414,8 +414,9 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  *              views of one packed projection.
  *   log_decay: fp32 [hv]; 0 forgets nothing, -inf everything but the token
  *              itself; a value above 0 grows the state (as the formula says)
- *   o:         bf16 [T][hv][128], dense; must not overlap an input or a state
- *              (GDR_ERR_ALIAS)
+ *   o:         bf16 [T][hv][128], dense
+ * No output (o, states, workspace) may overlap an input, log_decay, offsets and slots
+ * among them, or another output (GDR_ERR_ALIAS).
  * Precision: sums and states in fp32.  In the chunked form of the prefill the
  * probabilities (q.k) l^(i-j) and the state that a chunk's queries read go to the tensor
  * cores as two bf16 terms (16 bits of them; o itself has 8); the state that is returned
