@@ -421,6 +421,8 @@ bool meets_tables(const void *out, size_t bytes, const float *log_decay, int hv,
          overlaps(out, bytes, cu, (static_cast<size_t>(n) + 1) * 4);
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 int decay_prefill(const void *q, const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
                   const float *log_decay, float scale, int hk, int hv, const int32_t *cu_dev,
                   const int32_t *cu_host, int n_seqs, const DecayStates &st, void *o, void *workspace,
@@ -431,8 +433,8 @@ int decay_prefill(const void *q, const void *k, const void *v, int64_t qs, int64
   if (!cu_dev || !log_decay) return GDR_ERR_NULL;
   if (total > 0 && (!q || !k || !v || !o)) return GDR_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(st.h0) ||
-      !aligned16(st.hT) || !aligned16(st.pool) || !aligned16(workspace) ||
-      (reinterpret_cast<uintptr_t>(st.slot) & 3u) != 0)
+      !aligned16(st.hT) || !aligned16(st.pool) || !aligned16(workspace) || !aligned4(st.slot) ||
+      !aligned4(log_decay) || !aligned4(cu_dev))
     return GDR_ERR_ALIGN;
   const size_t o_bytes = static_cast<size_t>(total) * hv * kHeadDim * 2;
   const size_t need = decay_prefill_workspace_bytes(cu_host, n_seqs, hv);
@@ -459,7 +461,7 @@ int decay_decode(const void *q, const void *k, const void *v, int64_t qs, int64_
   int rc = decay_strides(hk, hv, &qs, &ks, &vs);
   if (rc) return rc;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(o) ||
-      (reinterpret_cast<uintptr_t>(slot) & 3u) != 0)
+      !aligned4(slot) || !aligned4(log_decay))
     return GDR_ERR_ALIGN;
   if (batch > 65535) return GDR_ERR_SHAPE;
   const size_t o_bytes = static_cast<size_t>(batch) * hv * kHeadDim * 2;

@@ -415,6 +415,8 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  *   log_decay: fp32 [hv]; 0 forgets nothing, -inf everything but the token
  *              itself; a value above 0 grows the state (as the formula says)
  *   o:         bf16 [T][hv][128], dense
+ * Tensors, states and workspace are 16-byte aligned, log_decay, offsets and slots
+ * 4-byte aligned (GDR_ERR_ALIGN).
  * No output (o, states, workspace) may overlap an input, log_decay, offsets and slots
  * among them, or another output (GDR_ERR_ALIAS).
  * Precision: sums and states in fp32.  In the chunked form of the prefill the

@@ -50,3 +50,13 @@ def test_outputs_on_the_tables_are_refused(L):
             for table in ("g", "slot") if slots else ("g",):
                 assert decode(L, slots, **{table: AT[name] + size - 4}) == 9, (slots, name, table)
                 assert decode(L, slots, **{table: AT[name] - 8}) == 9, (slots, name, table)
+
+
+def test_tables_off_their_alignment_are_refused(L):
+    """4-byte entries at an address that is not a multiple of 4: a load of them would fault."""
+    for slots in (False, True):
+        for by in (1, 2, 3):
+            for table in ("g", "cd", "slot") if slots else ("g", "cd"):
+                assert prefill(L, slots, **{table: AT[table] + by}) == 3, (slots, table)
+            for table in ("g", "slot") if slots else ("g",):
+                assert decode(L, slots, **{table: AT[table] + by}) == 3, (slots, table)
