@@ -18,7 +18,8 @@ __all__ = [
     "GdrError", "lib", "status_string", "prepare_chunks", "causal_conv", "chunk_prefill",
     "chunk_prefill_noalloc", "chunk_prefill_slots", "prefill_schedule", "prefill_workspace", "linear", "prefill_fused_workspace", "prefill_window",
     "decode_step", "decode_step_slots", "gated_rmsnorm", "get_device_error", "debug_wait_timeout",
-    "decay_attn_prefill", "decay_attn_prefill_slots", "decay_attn_workspace", "decay_attn_decode",
+    "decay_attn_prefill", "decay_attn_prefill_slots", "decay_attn_workspace",
+    "decay_attn_workspace_bound", "decay_attn_decode",
     "decay_attn_decode_slots", "block_norm",
     "HEAD_DIM", "CHUNK",
 ]
@@ -117,6 +118,8 @@ def lib(path: Optional[str] = None):
                                               ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp]
     L.gdr_decay_attn_prefill_workspace_size.restype = ctypes.c_size_t
     L.gdr_decay_attn_prefill_workspace_size.argtypes = [_vp, ctypes.c_int, ctypes.c_int]
+    L.gdr_decay_attn_prefill_workspace_bound.restype = ctypes.c_size_t
+    L.gdr_decay_attn_prefill_workspace_bound.argtypes = [i64, ctypes.c_int, ctypes.c_int]
     L.gdr_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), i64, i64, _vp]
     for fn in ("gdr_decay_attn_prefill", "gdr_decay_attn_prefill_slots", "gdr_decay_attn_decode",
                "gdr_decay_attn_decode_slots", "gdr_block_norm"):
@@ -593,6 +596,15 @@ def decay_attn_workspace(cu_seqlens_host, hv: int, device):
     torch = _torch()
     cu, _ = _host_cu(cu_seqlens_host)
     nbytes = int(lib().gdr_decay_attn_prefill_workspace_size(cu.ctypes.data, cu.shape[0] - 1, int(hv)))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def decay_attn_workspace_bound(max_tokens: int, max_seqs: int, hv: int, device):
+    """A torch uint8 device buffer that is enough for every decayed-attention prefill of at most
+    max_seqs sequences with max_tokens tokens together (the need of one call may exceed that of a
+    longer one), or None when none of them needs one."""
+    torch = _torch()
+    nbytes = int(lib().gdr_decay_attn_prefill_workspace_bound(int(max_tokens), int(max_seqs), int(hv)))
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 

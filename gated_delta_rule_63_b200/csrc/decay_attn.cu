@@ -109,6 +109,10 @@ constexpr uint32_t VT_TERM = C / 2, VT_BUF = 3 * VT_TERM;
 
 constexpr int kListed = 64;    // sequences whose offsets ride in the launch parameters
 constexpr int kMostSplit = 32; // sequences of a call that may be split into segments
+constexpr int kMostUnits = 2 * kSms;   // (sequence, head) pairs of such a call
+constexpr int kMostSegs = 32;  // segments of a sequence
+constexpr int kLeastSeg = 4;   // chunks of one that is not its sequence's last
+constexpr int kMostPieces = 2;
 
 struct DecayPrefillParams {
   const int32_t *cu;   // offsets in device memory, read when there are more than kListed sequences
@@ -903,7 +907,7 @@ int chunks_of(const int32_t *cu, int n) {
 // another launch (4) and the pieces' states for each later segment (0.6 for each).
 DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
   DecayPlan best{0, n_seqs, 0, 0, 0, 0};
-  if (n_seqs > kMostSplit || static_cast<int64_t>(n_seqs) * hv > 2 * kSms) return best;
+  if (n_seqs > kMostSplit || static_cast<int64_t>(n_seqs) * hv > kMostUnits) return best;
   int nc[kMostSplit];
   for (int n = 0; n < n_seqs; ++n) nc[n] = chunks_of(cu, n);
   std::sort(nc, nc + n_seqs, [](int a, int b) { return a > b; });
@@ -913,9 +917,9 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
   int64_t load = 0;
   for (int n = 0; n < n_seqs; ++n) load += static_cast<int64_t>(nc[n]) * hv;
   if (least <= 1.1 * static_cast<double>(load) / kSms) return best;   // no SM is idle for long
-  for (int s = 2; s <= 32; ++s) {
+  for (int s = 2; s <= kMostSegs; ++s) {
     const int len = (nc[0] + s - 1) / s;
-    if (len < 4) break;
+    if (len < kLeastSeg) break;
     int units = 0;
     for (int n = 0; n < n_seqs; ++n) units += std::max(1, (nc[n] + len - 1) / len);
     const int split = units - n_seqs;
@@ -928,7 +932,7 @@ DecayPlan plan_decay(const int32_t *cu, int n_seqs, int hv) {
     const double base = main.time() + 4.0;
     // an early segment whole, or as two thirds and a third, which two thirds of 148 SMs and the rest
     // take side by side (32 768 tokens, 48 heads: 481 us whole, 461 us in pieces)
-    for (int part : {len, (2 * len + 2) / 3}) {
+    for (int part : {len, (2 * len + 2) / 3}) {   // (kMostPieces)
       const int pieces = (len + part - 1) / part;
       Launch state;
       for (int i = 0; i < pieces; ++i) state.add(split * hv, 0.42 * std::min(part, len - i * part));
@@ -958,6 +962,14 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, ui
 size_t decay_prefill_workspace_bytes(const int32_t *cu, int n_seqs, int hv) {
   const DecayPlan plan = plan_decay(cu, n_seqs, hv);
   return plan.seg_chunks == 0 ? 0 : static_cast<size_t>(plan.slots) * hv * D * D * sizeof(float);
+}
+
+// A state for each sequence and each piece of an early segment; of these a sequence has less than
+// kMostSegs, and all together at most one for every kLeastSeg chunks.
+size_t decay_prefill_workspace_bound(int64_t tokens, int n_seqs, int hv) {
+  const int64_t n = std::min({n_seqs, kMostSplit, kMostUnits / hv});
+  const int64_t early = std::min<int64_t>(n * (kMostSegs - 1), (tokens / C + n) / kLeastSeg);
+  return early <= 0 ? 0 : static_cast<size_t>(kMostPieces * early + n) * hv * D * D * sizeof(float);
 }
 
 int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,

@@ -482,6 +482,11 @@ size_t gdr_decay_attn_prefill_workspace_size(const int32_t *cu_host, int n_seqs,
   return decay_prefill_workspace_bytes(cu_host, n_seqs, hv);
 }
 
+size_t gdr_decay_attn_prefill_workspace_bound(int64_t max_tokens, int max_seqs, int hv) {
+  if (max_tokens < 0 || max_tokens > INT32_MAX || max_seqs <= 0 || hv <= 0) return 0;
+  return decay_prefill_workspace_bound(max_tokens, max_seqs, hv);
+}
+
 int gdr_decay_attn_prefill(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                            int64_t v_stride, const float *log_decay, float scale, int hk, int hv,
                            const int32_t *cu_dev, const int32_t *cu_host, int n_seqs, const float *h0, float *hT,

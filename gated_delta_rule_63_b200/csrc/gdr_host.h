@@ -121,6 +121,8 @@ int launch_decay_prefill(const void *q, const void *k, const void *v, int64_t q_
                          void *o, void *workspace, cudaStream_t s);
 // bytes of workspace a prefill of these sequences runs on (0: none)
 size_t decay_prefill_workspace_bytes(const int32_t *cu_host, int n_seqs, int hv);
+// bytes that are enough for every prefill of so many tokens and sequences
+size_t decay_prefill_workspace_bound(int64_t tokens, int n_seqs, int hv);
 int launch_decay_decode(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const float *log_decay, float scale, int hk, int hv, float *state,
                         const int32_t *slot, int n_slots, void *o, int batch, cudaStream_t s);

@@ -450,9 +450,19 @@ GDR_API int gdr_decay_attn_prefill(const void *q, const void *k, const void *v, 
 /*
  * Bytes of workspace a prefill of these sequences needs: 0 unless sequences are
  * split into segments that run beside each other (few heads and sequences for the
- * GPU), whose states it then holds.  Host only.  0 for invalid arguments.
+ * GPU), whose states it then holds.  Host only.  0 for invalid arguments.  A longer
+ * sequence may need less than a shorter one (it is cut otherwise): the size of the
+ * longest call does not cover the others, gdr_decay_attn_prefill_workspace_bound does.
  */
 GDR_API size_t gdr_decay_attn_prefill_workspace_size(const int32_t *cu_seqlens_host, int n_seqs, int hv);
+
+/*
+ * Bytes of workspace that are enough for every prefill of at most max_seqs sequences
+ * with at most max_tokens tokens together and hv value heads: for a buffer made once
+ * and kept.  Several times what a call needs as a rule.  Host only.  0 for invalid
+ * arguments.
+ */
+GDR_API size_t gdr_decay_attn_prefill_workspace_bound(int64_t max_tokens, int max_seqs, int hv);
 
 /*
  * gdr_decay_attn_prefill_slots -- the same on a pool of cached states.  Sequence n
