@@ -84,3 +84,24 @@ def test_o_is_not_too_small(decay):
     off = o.double() - ref.to(torch.bfloat16).double()
     shift = float((off * ref).sum() / (ref * ref).sum())
     assert abs(shift) <= 16 * E
+
+
+@pytest.mark.parametrize("others", [0, 33])
+def test_state_in_the_mean_over_a_head(others):
+    """The returned state's error in the Frobenius norm, head by head, slow ones included; in segments, and
+    (behind 33 short sequences) in one piece.
+
+    Random values: the errors of a head's elements add as squares, and each source is relative to the
+    state's own size.  Factors and products of V': 1.2 e.  A chunk's sums, should they be cut off: e / 2
+    in the mean for four products at full size, 1.6 e.  The state's own two roundings a chunk, 0.41 e
+    each time, over the 1 / (128 |g|) <= 16 chunks that it remembers: 1.6 e.  The decay of a chunk, good to
+    e (1 - l^64) and |64 g| e / 2, of one sign, over the same memory: 0.75 e.  Together under 6 e = 7.2e-7;
+    two terms of V' would leave 5e-6 to 1e-5."""
+    q, k, v, cu, _ = make(53, [1] * others + [1500], 1, 5)
+    g = np.array([-0.5, -0.06, -0.01, -0.004, -0.0005], np.float32)
+    assert (G.decay_attn_workspace(cu, 5, "cuda") is not None) == (others == 0)
+    _, hT = run(q, k, v, g, cu)
+    _, ref = O.decay_attn(q, k, v, g, cu)
+    err = hT[-1].double().cpu().numpy() - ref[-1]
+    off = np.sqrt((err ** 2).sum((1, 2)) / (ref[-1] ** 2).sum((1, 2)))
+    assert off.max() <= 6 * E, off
