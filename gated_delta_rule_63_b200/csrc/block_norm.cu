@@ -13,8 +13,13 @@
 // shuffles alone (16 384 rows of 512: 9.9 us, 17.5 us with a CTA a row); above, a CTA of up to
 // 512 threads does (64 rows of 1024: 2.1 us, 2.7 us with a warp a row; 16 384 rows 20.4 and
 // 20.6 us), 16 values a thread up to 8192 (4096 rows of 8192: 41.4 us, 49.1 us with 8 values
-// a thread; of 5120 26.9, with 8 values 29.8, with 32 27.2 us), 32 up to 16384, 64 above.
-// Residual + norm of 4096 x 5120 bf16 in 26.9 us moves 168 MB, 6.2 TB/s: 95% of a copy's rate.
+// a thread; of 5120 26.9, with 8 values 29.8, with 32 27.2 us), 32 up to 16384 (2048 rows of 16 384
+// with everything and an fp32 residual: 94 us, 130 us with 64 values; residual and norm alone 45 and
+// 49 us; of 8192 33.6 million values so: 16 values 82 us, 32 86 us), 64 above, the only form whose 512
+// threads reach 32 768.  That one needs more registers than a thread has (up to 228 bytes go to local
+// memory and come back) and takes 56 to 69 us for 33.6 million values, with everything 138 to 183 us.
+// Residual + norm of 4096 x 5120 bf16 in 28 us moves 168 MB, 6.0 TB/s: 91% of a copy's rate; with the
+// residual in fp32 40.8 us, 252 MB: 94%, with both norms and a row's gate 52 us, 294 MB: 86%.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -16,20 +16,21 @@
 //     PV  = V^T P^T               M = 128 (dv),     N = 64,  K = 64;  P in two bf16 terms
 // q, k, v are bf16 and exact.  H0 and P (fp32) as hi + lo bf16 keep 16 bits of them, an error
 // far below o's own rounding to bf16; V' keeps 24 bits (hi + mid + lo), so the state is an fp32 sum in
-// every chunk: the final one's error is 0.7e-7 to 1.0e-7.  Two terms, the second one cut off, leave
-// each value up to 2^-15 too small.  Without the third one in chunks far back, the final state was wrong
-// wherever the tokens after them add nothing (a masked tail); without it in segments whose state is
-// read by o alone, o came out 5e-6 to 6e-6 too small (32 768 tokens of 48 heads in 443 instead of 452 us).
+// every chunk: the final one's error is 0.6e-7 to 1.2e-7 (rel-L2).  Two terms, the second one cut off,
+// leave each value up to 2^-15 too small.  Without the third one in chunks far back, the final state was
+// wrong wherever the tokens after them add nothing (a masked tail); without it in segments whose state
+// is read by o alone, o came out 2e-6 to 5e-6 too small (32 768 tokens of 48 heads in 443, with it 452 us).
 //
 // V' and H0 are A operands in tensor memory, written from registers: as shared-memory tiles they
 // took the bandwidth that the products read their operands with (149 -> 92 us for a prompt of 4096
 // tokens and 48 value heads, with o and V going through 8 x 8 transposes).
 //
 // What bounds it: the products of a chunk, 13.6 MFLOP (44 MMAs), keep the tensor pipe
-// for 2900 of a chunk's 3090 cycles (an M = 128, N = 64, K = 16 product with A in tensor
+// for 2900 of a chunk's ~3150 cycles (an M = 128, N = 64, K = 16 product with A in tensor
 // memory takes 70 cycles, N = 128 79), and S -> P -> PV -> o -> the next S, which share columns, is
-// a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 65 to 67 us; 32 768
-// tokens take 413 to 430 us, 1.08 GB read and written once at 2.5 to 2.6 TB/s, at the power cap.
+// a chain of about that length.  A prompt of 4096 tokens and 48 value heads takes 66 to 67 us; 32 768
+// tokens take 443 us, 1.08 GB read and written once at 2.4 TB/s, and 505 us without a pause, at the
+// power cap.
 //
 // One CTA (16 warps, the last two idle) walks the chunks of one (value head, sequence or segment):
 //   warps 0..3   P from S (TMEM -> registers -> shared memory), and o from OI and PV
@@ -61,8 +62,8 @@
 // run beside each other: a first launch (kOut = false: K and V only) leaves what each segment
 // but the last adds to the state, a second one starts every segment from the decayed sum of
 // those before it.  plan_decay() weighs the extra pass against the shorter chain; measured, in
-// one piece and as it chooses: 512 tokens of 48 value heads 19.4 (not cut), 1024 32.6 and 26.4,
-// 4096 112 and 65, 16 384 413 and 212 us; 4096 of 16 heads 111 and 41, 8192 of 2 213 and 38.6 us.
+// one piece and as it chooses: 512 tokens of 48 value heads 20 (not cut), 1024 33 and 27.4, 4096 109
+// and 66, 16 384 416 and 224, 32 768 824 and 443 us; 4096 of 16 heads 108 and 41, 8192 of 2 208 and 38 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

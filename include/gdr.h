@@ -78,7 +78,8 @@ GDR_API const char *gdr_status_string(int status);
  * gdr_chunk_prefill_fused_workspace_size; 3: gdr_decode_step_slots; 4:
  * gdr_chunk_prefill_slots; 5: gdr_chunk_prefill_schedule and the
  * pipelined window schedule; 6: gdr_linear).  The calls of decayed linear
- * attention and gdr_block_norm were added under 6: they change no other call. */
+ * attention and gdr_block_norm came later under 6: they change no other call, and a
+ * program that has to know looks the symbols up. */
 GDR_API int gdr_abi_version(void);
 
 /*
@@ -413,17 +414,22 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  *              A stride is at least a row and a multiple of 8, so q, k, v may be
  *              views of one packed projection.
  *   log_decay: fp32 [hv]; 0 forgets nothing, -inf everything but the token
- *              itself; a value above 0 grows the state (as the formula says)
+ *              itself; a value above 0 grows the state (as the formula says).  The
+ *              prefill uses powers of l up to l^64: they must stay within fp32's
+ *              range (log_decay <= 1.38), or zeros in v times an infinity become NaN
  *   o:         bf16 [T][hv][128], dense
  * Tensors, states and workspace are 16-byte aligned, log_decay, offsets and slots
  * 4-byte aligned (GDR_ERR_ALIGN).
  * No output (o, states, workspace) may overlap an input, log_decay, offsets and slots
- * among them, or another output (GDR_ERR_ALIAS).
- * Precision: sums and states in fp32.  In the chunked form of the prefill the
- * probabilities (q.k) l^(i-j) and the state that a chunk's queries read go to the tensor
- * cores as two bf16 terms (16 bits of them; o itself has 8); the state that is returned
- * has the error of fp32 sums.  A value that is not finite makes its sequence's later outputs and its state not
- * finite; earlier tokens' outputs and other sequences keep theirs.
+ * among them, or another output (GDR_ERR_ALIAS); states may be updated in place.
+ * Precision: sums and states in fp32, also the state inside a prompt and the one that is
+ * returned (of values below 2^-110 the prefill keeps what lies above 2^-133).  In the
+ * chunked form of the prefill the probabilities (q.k) l^(i-j), and the copy of the state
+ * that a chunk's queries are multiplied with, go to the tensor cores as two bf16 terms:
+ * 16 bits of them, where o itself has 8.
+ * A value that is not finite makes what the formula makes of it not finite (q its token's
+ * o, v its column of the later o and of the state, k all later o); earlier tokens' outputs
+ * and other sequences keep theirs.
  */
 
 /*
