@@ -415,8 +415,9 @@ GDR_API int gdr_gated_rmsnorm(const void *o, const void *z, const float *w, floa
  *              views of one packed projection.
  *   log_decay: fp32 [hv]; 0 forgets nothing, -inf everything but the token
  *              itself; a value above 0 grows the state (as the formula says).  The
- *              prefill uses powers of l up to l^64: they must stay within fp32's
- *              range (log_decay <= 1.38), or zeros in v times an infinity become NaN
+ *              prefill uses powers of l up to l^64 and scale l^(i-j) (q.k) inside 64
+ *              tokens: both must stay within fp32's range (l^64 does to log_decay =
+ *              1.38), or zeros in v times an infinity become NaN
  *   o:         bf16 [T][hv][128], dense
  * Tensors, states and workspace are 16-byte aligned, log_decay, offsets and slots
  * 4-byte aligned (GDR_ERR_ALIGN).

@@ -105,3 +105,19 @@ def test_state_in_the_mean_over_a_head(others):
     err = hT[-1].double().cpu().numpy() - ref[-1]
     off = np.sqrt((err ** 2).sum((1, 2)) / (ref[-1] ** 2).sum((1, 2)))
     assert off.max() <= 6 * E, off
+
+
+def test_state_of_the_smallest_values():
+    """One chunk, one key a row, values from 2^-133 (bf16's least) to 2^-105: the bound of one product, and
+    what lies below bf16's least step."""
+    q, k, v, cu, _ = make(54, [64], 1, 2)
+    k[:] = 0.0
+    k[np.arange(64), 0, np.arange(64)] = 1.0
+    v = O.round_bf16_f64(np.sign(v) * 2.0 ** np.random.default_rng(5).uniform(-133, -105, v.shape))
+    g = np.array([0.0, -0.01], np.float32)
+    _, hT = run(q, k, v, g, cu)
+    _, ref = O.decay_attn(q, k, v, g, cu)
+    err = np.abs(hT.double().cpu().numpy() - ref)
+    bound = (6 + np.abs(g.astype(np.float64)) * 64 / 2)[None, :, None, None] * E * np.abs(ref) + 2.0 ** -133
+    assert bool(np.all(err <= bound)), float(np.max(err / bound))
+    assert bool(np.all(err[:, 0] == 0.0))                  # nothing decays: the values themselves
